@@ -60,7 +60,8 @@ extern "C" {
 typedef enum {
     MSSM_F32 = 0,
     MSSM_BF16 = 1,
-    MSSM_I32 = 2  /* index tensors only (cu_seqlens) */
+    MSSM_I32 = 2, /* index tensors (cu_seqlens) and packed 4-bit weights */
+    MSSM_U8 = 3   /* 4-bit codes (two per byte) and zero points */
 } mssm_dtype;
 
 typedef enum {
@@ -303,6 +304,109 @@ mssm_status mssm_causal_conv1d_fwd(const mssm_tensor *x, const mssm_tensor *weig
 mssm_status mssm_causal_conv1d_update(mssm_tensor *conv_state, const mssm_tensor *x, const mssm_tensor *weight,
                                       const mssm_tensor *bias, int silu_flag, mssm_tensor *out, void *stream);
 
+/*
+ * The real-gated linear recurrence: one state per channel, whose decay is set by a
+ * learned rate and a recurrence gate and whose input passes an input gate and is
+ * normalised by the decay.  It takes the selective scan's place in a recurrent block:
+ * behind mssm_causal_conv1d_fwd, in front of the silu gate.
+ *
+ *   r_t = sigmoid(r_raw_t + r_bias_d),  i_t = sigmoid(i_raw_t + i_bias_d)
+ *   a_t = exp(-decay_scale * softplus(lam_d) * r_t)
+ *   h_t = a_t h_(t-1) + sqrt(1 - a_t^2) * i_t * x_t          (h_(-1) = h0, default 0)
+ *   out_t = h_t * silu(z_t)                                  (z optional)
+ *
+ *   x, r, i, z   [Bt, D, L]  bf16|f32 (one dtype; z NULL: no gate), L stride 1
+ *   lam          [D] f32;  r_bias, i_bias [D] f32 or NULL
+ *   out          [Bt, D, L]  dtype of x, written
+ *   last_state   [S, D]      f32 or NULL: h after the last step, written
+ * S = Bt, or the number of packed sequences.  Rows may start on any element: whole
+ * 16-byte vectors are used where the rows of all tensors lie equally far from a 16-byte
+ * boundary (as those of equally shaped dense tensors do), single elements elsewhere.
+ *
+ * Options of mssm_gated_scan_fwd and _bwd (ext NULL: decay_scale 8, no others).  Set
+ * struct_size to sizeof(mssm_gated_ext); fields may be appended in later versions.
+ *   decay_scale  positive and finite
+ *   h0           [S, D] f32: the state before the first step of each sequence (NULL: zero)
+ *   cu_seqlens   [S + 1] int32 DEVICE offsets, or NULL: packed sequences of a [1, D, T]
+ *                row; sequence s covers steps cu_seqlens[s] .. cu_seqlens[s+1] - 1.  An
+ *                empty sequence's last state is its h0.  Steps outside every sequence are
+ *                left unwritten.  Offsets outside [0, T] or decreasing ones are reported as
+ *                MSSM_ERR_INVALID_ARG by mssm_get_error; the outputs are then undefined.
+ * No workspace, and the same inputs in rows equally far from a 16-byte boundary give the
+ * same bits.  L below 2^31 - 2^16.
+ */
+typedef struct {
+    int32_t struct_size;
+    float decay_scale;
+    const mssm_tensor *h0;
+    const mssm_tensor *cu_seqlens;
+} mssm_gated_ext;
+
+mssm_status mssm_gated_scan_fwd(const mssm_tensor *x, const mssm_tensor *r, const mssm_tensor *i,
+                                const mssm_tensor *lam, const mssm_tensor *r_bias, const mssm_tensor *i_bias,
+                                const mssm_tensor *z, const mssm_gated_ext *ext, mssm_tensor *out,
+                                mssm_tensor *last_state, void *stream);
+
+/*
+ * Backward of mssm_gated_scan_fwd with the same inputs and options, given
+ * dout = dLoss/dout and, optionally, dlast_state = dLoss/dlast_state:
+ *   dx, dr, di       [Bt, D, L] dtype of x, written (dr, di: before bias and sigmoid)
+ *   dz               [Bt, D, L] dtype of x, given exactly when z is
+ *   dlam             [D] f32;  dr_bias, di_bias [D] f32, given exactly when the biases are
+ *   dh0              [S, D] f32 or NULL (also without h0: the gradient at the zero state)
+ *   workspace        [3, Bt, D] f32, dense: the rows' parts of dlam and the biases'
+ *                    gradients, which are then added in batch order; NULL when Bt is 1
+ * The states are recomputed, never stored.  Gradients at steps outside every packed
+ * sequence are left unwritten.  Bits as for the forward scan.  L may reach 2^23.
+ */
+mssm_status mssm_gated_scan_bwd(const mssm_tensor *x, const mssm_tensor *r, const mssm_tensor *i,
+                                const mssm_tensor *lam, const mssm_tensor *r_bias, const mssm_tensor *i_bias,
+                                const mssm_tensor *z, const mssm_gated_ext *ext, const mssm_tensor *dout,
+                                const mssm_tensor *dlast_state, mssm_tensor *dx, mssm_tensor *dr, mssm_tensor *di,
+                                mssm_tensor *dz, mssm_tensor *dlam, mssm_tensor *dr_bias, mssm_tensor *di_bias,
+                                mssm_tensor *dh0, mssm_tensor *workspace, void *stream);
+
+/*
+ * One decode step of the recurrence, state updated IN PLACE:
+ *   state [Bt, D] f32;  x, r, i, z, out [Bt, D] bf16|f32 (z NULL: no gate), any strides
+ * Steps from a zero state reproduce mssm_gated_scan_fwd step by step.
+ */
+mssm_status mssm_gated_state_update(mssm_tensor *state, const mssm_tensor *x, const mssm_tensor *r,
+                                    const mssm_tensor *i, const mssm_tensor *lam, const mssm_tensor *r_bias,
+                                    const mssm_tensor *i_bias, const mssm_tensor *z, float decay_scale,
+                                    mssm_tensor *out, void *stream);
+
+/*
+ * Linear maps with 4-bit weights and group scales, for the projections around a decode
+ * step (a few tokens, where the product is the stream of its weights):
+ *
+ *   out[m,n] = sum_k x[m,k] * scale[n, k/group] * (code[n,k] - zero[n, k/group]) + bias[n]
+ *
+ * mssm_w4_pack lays a weight out once in the order in which the product reads it:
+ *   codes    [N, (K + 1) / 2] u8: input 2j in the low nibble of byte j, 2j + 1 in the high
+ *   scales   [N, G] f32|bf16, G = ceil(K / group); the last group may be short
+ *   zeros    [N, G] u8, values 0..15, or NULL: 8 everywhere
+ *   group    a positive multiple of 32
+ *   qweight, qscales, qzeros: dense 1-dim i32, dtype of scales, u8 (given exactly when
+ *            zeros is), of the sizes that mssm_w4_packed_sizes returns
+ * mssm_w4_linear multiplies:
+ *   x        [M, K] bf16|f32, K stride 1;  out [M, N] dtype of x, any strides
+ *   bias     [N] f32 or NULL
+ *   N, K, group as packed (K and N are read from x and out)
+ * Every group's sum and the sum over the groups are fp32; the products are exact.  The
+ * inputs are split over warps, and for few outputs over the CTAs of a cluster, whose sums
+ * are added in a fixed order: the same inputs give the same bits.  Any M is taken; the
+ * kernels are laid out for a few tokens, and re-read the weight for every 32 of them.
+ * K and N at least 1 and below 2^31 - 64.
+ */
+mssm_status mssm_w4_packed_sizes(int64_t N, int64_t K, int64_t group, int64_t *qweight, int64_t *qscales);
+mssm_status mssm_w4_pack(const mssm_tensor *codes, const mssm_tensor *scales, const mssm_tensor *zeros, int64_t K,
+                         int64_t group, mssm_tensor *qweight, mssm_tensor *qscales, mssm_tensor *qzeros,
+                         void *stream);
+mssm_status mssm_w4_linear(const mssm_tensor *x, const mssm_tensor *qweight, const mssm_tensor *qscales,
+                           const mssm_tensor *qzeros, int64_t group, const mssm_tensor *bias, mssm_tensor *out,
+                           void *stream);
+
 /* Static, human-readable name of a status code. */
 const char *mssm_status_string(mssm_status status);
 
@@ -434,7 +538,13 @@ typedef enum {
     MSSM_KERNEL_STATE_UPDATE = 2,     /* decode step */
     MSSM_KERNEL_CONV = 3,             /* causal conv1d (prefill and decode step) */
     MSSM_KERNEL_SCAN_BWD = 4,         /* backward scan (both of its passes) */
-    MSSM_KERNEL_KINDS = 5
+    MSSM_KERNEL_KINDS = 5,            /* the kinds of mssm_kernel_stats */
+    /* counted by mssm_kernel_stats_all only */
+    MSSM_KERNEL_GATED_SCAN = 5,  /* gated recurrence, forward */
+    MSSM_KERNEL_GATED_BWD = 6,   /* gated recurrence, backward (and the sum of its row sums) */
+    MSSM_KERNEL_GATED_STEP = 7,  /* gated recurrence, decode step */
+    MSSM_KERNEL_W4_LINEAR = 8,   /* 4-bit linear map (and the layout of its weight) */
+    MSSM_KERNEL_KINDS_ALL = 9
 } mssm_kernel_kind;
 
 /*
@@ -446,6 +556,9 @@ typedef enum {
  * counters afterwards.
  */
 mssm_status mssm_kernel_stats(int64_t *launches, int64_t *timed, double *ms, int reset);
+
+/* The same for the first `kinds` kinds, at most MSSM_KERNEL_KINDS_ALL: the arrays have `kinds` elements. */
+mssm_status mssm_kernel_stats_all(int kinds, int64_t *launches, int64_t *timed, double *ms, int reset);
 
 /*
  * Frees the library's per-device workspaces and forgets the device addresses it

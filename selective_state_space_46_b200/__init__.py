@@ -12,6 +12,8 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
+import threading
 from typing import Optional, Tuple
 
 import torch
@@ -26,6 +28,9 @@ __all__ = [
     "mssm_selective_scan_fwd_ex", "MSSM_DISC_EULER", "MSSM_DISC_ZOH",
     "mssm_causal_conv1d_fwd", "mssm_causal_conv1d_update", "causal_conv1d", "causal_conv1d_update",
     "mssm_selective_scan_bwd", "selective_scan_bwd",
+    "mssm_gated_scan_fwd", "mssm_gated_scan_bwd", "mssm_gated_state_update",
+    "gated_scan_fwd", "gated_scan_bwd", "gated_state_update",
+    "mssm_w4_pack", "mssm_w4_linear", "W4Weight", "w4_pack", "w4_linear",
     "KERNEL_KINDS",
 ]
 
@@ -46,7 +51,8 @@ MSSM_OPT_ROWS_PER_THREAD = 8
 MSSM_DISC_EULER, MSSM_DISC_ZOH = 0, 1
 SCHEDULES = {"forward": 1, "summaries+forward": 2, "chained": 3, "fused": 4, "split": 5}
 DECODE_PATHS = {"stream": 1, "bulk_tile": 2, "per_row": 3}
-KERNEL_KINDS = ("scan_chunk_state", "scan_out", "state_update", "conv", "scan_bwd")
+KERNEL_KINDS = ("scan_chunk_state", "scan_out", "state_update", "conv", "scan_bwd", "gated_scan", "gated_bwd",
+                "gated_step", "w4_linear")
 
 
 class mssm_tensor(ctypes.Structure):
@@ -88,9 +94,22 @@ _lib.mssm_set_option.argtypes = [ctypes.c_int, ctypes.c_int64]
 _lib.mssm_set_option.restype = ctypes.c_int
 _lib.mssm_shutdown.restype = ctypes.c_int
 _lib.mssm_version.restype = ctypes.c_char_p
-_lib.mssm_kernel_stats.argtypes = [ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_int64),
-                                   ctypes.POINTER(ctypes.c_double), ctypes.c_int]
-_lib.mssm_kernel_stats.restype = ctypes.c_int
+_lib.mssm_kernel_stats_all.argtypes = [ctypes.c_int, ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_int64),
+                                       ctypes.POINTER(ctypes.c_double), ctypes.c_int]
+_lib.mssm_kernel_stats_all.restype = ctypes.c_int
+# the entry points below take descriptor addresses from _Descs
+_lib.mssm_gated_scan_fwd.argtypes = [_V] * 11
+_lib.mssm_gated_scan_fwd.restype = ctypes.c_int
+_lib.mssm_gated_scan_bwd.argtypes = [_V] * 20
+_lib.mssm_gated_scan_bwd.restype = ctypes.c_int
+_lib.mssm_gated_state_update.argtypes = [_V] * 8 + [ctypes.c_float, _V, _V]
+_lib.mssm_gated_state_update.restype = ctypes.c_int
+_lib.mssm_w4_packed_sizes.argtypes = [ctypes.c_int64] * 3 + [ctypes.POINTER(ctypes.c_int64)] * 2
+_lib.mssm_w4_packed_sizes.restype = ctypes.c_int
+_lib.mssm_w4_pack.argtypes = [_V] * 3 + [ctypes.c_int64] * 2 + [_V] * 4
+_lib.mssm_w4_pack.restype = ctypes.c_int
+_lib.mssm_w4_linear.argtypes = [_V] * 4 + [ctypes.c_int64] + [_V] * 3
+_lib.mssm_w4_linear.restype = ctypes.c_int
 _lib.mssm_scan_plan.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int,
                                 ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int64),
                                 ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_int)]
@@ -118,8 +137,8 @@ class MssmError(RuntimeError):
         self.status = status
 
 
-MSSM_I32 = 2
-_DT = {torch.float32: MSSM_F32, torch.bfloat16: MSSM_BF16, torch.int32: MSSM_I32}
+MSSM_I32, MSSM_U8 = 2, 3
+_DT = {torch.float32: MSSM_F32, torch.bfloat16: MSSM_BF16, torch.int32: MSSM_I32, torch.uint8: MSSM_U8}
 
 
 def _desc(t: Optional[torch.Tensor]):
@@ -180,7 +199,7 @@ def mssm_kernel_stats(reset: bool = False) -> dict:
     launches = (ctypes.c_int64 * n)()
     timed = (ctypes.c_int64 * n)()
     ms = (ctypes.c_double * n)()
-    _check(_lib.mssm_kernel_stats(launches, timed, ms, int(reset)))
+    _check(_lib.mssm_kernel_stats_all(n, launches, timed, ms, int(reset)))
     return {k: {"launches": launches[i], "timed": timed[i], "ms": ms[i]} for i, k in enumerate(KERNEL_KINDS)}
 
 
@@ -289,6 +308,127 @@ def mssm_causal_conv1d_update(conv_state, x, weight, bias, out, silu_flag=True, 
                                           _stream(stream, x)))
 
 
+class _Descs(threading.local):
+    """A thread's block of ``mssm_tensor`` descriptors, written in place: a decode step is a few
+    microseconds on the GPU, so the marshalling of its arguments is kept short."""
+    MOST = 20
+    LAYOUT = struct.Struct("qii8q")
+
+    def __init__(self):
+        self.block = ctypes.create_string_buffer(self.MOST * ctypes.sizeof(mssm_tensor))
+        self.base = ctypes.addressof(self.block)
+
+    def __call__(self, *tensors):
+        """Descriptor addresses (None for None), valid until the thread's next call."""
+        out = []
+        at, block, pack, base = 0, self.block, self.LAYOUT.pack_into, self.base
+        for t in tensors:
+            if t is None:
+                out.append(None)
+                continue
+            shape, stride = t.shape, t.stride()
+            n = len(shape)
+            if n == 3:
+                pack(block, at, t.data_ptr(), _DT.get(t.dtype, -1), 3, *shape, 0, *stride, 0)
+            elif n == 2:
+                pack(block, at, t.data_ptr(), _DT.get(t.dtype, -1), 2, *shape, 0, 0, *stride, 0, 0)
+            elif n == 1:
+                pack(block, at, t.data_ptr(), _DT.get(t.dtype, -1), 1, shape[0], 0, 0, 0, stride[0], 0, 0, 0)
+            else:
+                raise ValueError("tensors have 1 to 3 dims here")
+            out.append(base + at)
+            at += 80
+        return out
+
+
+assert _Descs.LAYOUT.size == ctypes.sizeof(mssm_tensor) == 80
+_descs = _Descs()
+
+
+class mssm_gated_ext(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_int32), ("decay_scale", ctypes.c_float),
+                ("h0", ctypes.c_void_p), ("cu_seqlens", ctypes.c_void_p)]
+
+
+def _on(stream, x, *tensors):
+    """The raw stream of a call on the tensors' device, which is made current for it."""
+    device = x.device
+    if device.type != "cuda":
+        raise ValueError("this operator runs on CUDA tensors only")
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"all tensors must be on {device} (got one on {t.device})")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _call(device, fn, *args):
+    if torch._C._cuda_getDevice() == device.index:
+        _check(fn(*args))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args))
+
+
+class _allocating_on:
+    """Tensors allocated here belong to the stream that the call runs on."""
+
+    def __init__(self, stream, device):
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        self.guard = None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def mssm_gated_scan_fwd(x, r, i, lam, r_bias, i_bias, z, out, last_state, decay_scale=8.0, h0=None, cu_seqlens=None,
+                        stream=None) -> None:
+    """Marshal torch tensors into ``mssm_gated_scan_fwd`` (see include/mssm.h)."""
+    s = _on(stream, x, r, i, lam, r_bias, i_bias, z, out, last_state, h0, cu_seqlens)
+    d = _descs(x, r, i, lam, r_bias, i_bias, z, out, last_state, h0, cu_seqlens)
+    ext = mssm_gated_ext(ctypes.sizeof(mssm_gated_ext), decay_scale, d[9], d[10])
+    _call(x.device, _lib.mssm_gated_scan_fwd, *d[:7], ctypes.addressof(ext), d[7], d[8], s)
+
+
+def mssm_gated_scan_bwd(x, r, i, lam, r_bias, i_bias, z, dout, dlast_state, dx, dr, di, dz, dlam, dr_bias, di_bias,
+                        dh0, workspace, decay_scale=8.0, h0=None, cu_seqlens=None, stream=None) -> None:
+    """Marshal torch tensors into ``mssm_gated_scan_bwd`` (see include/mssm.h)."""
+    ts = (x, r, i, lam, r_bias, i_bias, z, dout, dlast_state, dx, dr, di, dz, dlam, dr_bias, di_bias, dh0, workspace,
+          h0, cu_seqlens)
+    s = _on(stream, *ts)
+    d = _descs(*ts)
+    ext = mssm_gated_ext(ctypes.sizeof(mssm_gated_ext), decay_scale, d[18], d[19])
+    _call(x.device, _lib.mssm_gated_scan_bwd, *d[:7], ctypes.addressof(ext), *d[7:18], s)
+
+
+def mssm_gated_state_update(state, x, r, i, lam, r_bias, i_bias, z, out, decay_scale=8.0, stream=None) -> None:
+    """Marshal torch tensors into ``mssm_gated_state_update`` (state updated in place)."""
+    s = _on(stream, x, state, r, i, lam, r_bias, i_bias, z, out)
+    d = _descs(state, x, r, i, lam, r_bias, i_bias, z, out)
+    _call(x.device, _lib.mssm_gated_state_update, *d[:8], decay_scale, d[8], s)
+
+
+def mssm_w4_pack(codes, scales, zeros, in_features, group_size, qweight, qscales, qzeros, stream=None) -> None:
+    """Marshal torch tensors into ``mssm_w4_pack`` (see include/mssm.h)."""
+    s = _on(stream, codes, scales, zeros, qweight, qscales, qzeros)
+    d = _descs(codes, scales, zeros, qweight, qscales, qzeros)
+    _call(codes.device, _lib.mssm_w4_pack, *d[:3], in_features, group_size, *d[3:], s)
+
+
+def mssm_w4_linear(x, qweight, qscales, qzeros, group_size, bias, out, stream=None) -> None:
+    """Marshal torch tensors into ``mssm_w4_linear`` (see include/mssm.h)."""
+    s = _on(stream, x, qweight, qscales, qzeros, bias, out)
+    d = _descs(x, qweight, qscales, qzeros, bias, out)
+    _call(x.device, _lib.mssm_w4_linear, *d[:4], group_size, d[4], d[5], s)
+
+
 # --------------------------------------------------------------------------
 # allocation conveniences (torch allocates; the library computes)
 # --------------------------------------------------------------------------
@@ -347,4 +487,95 @@ def state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus=T
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
     mssm_state_update_ex(state, x, dt, A, B, C, D, z, dt_bias, softplus, out,
                          discretization=MSSM_DISC_ZOH if zoh else MSSM_DISC_EULER, stream=stream)
+    return out
+
+
+def gated_scan_fwd(x, r, i, lam, r_bias=None, i_bias=None, z=None, c=8.0, h0=None, cu_seqlens=None, out=None,
+                   last_state=None, return_last_state=True,
+                   stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """The real-gated linear recurrence over ``x`` [Bt, D, L] with recurrence gate ``r`` and input gate
+    ``i`` (both before bias and sigmoid), decay rate ``c * softplus(lam)`` and optional silu gate ``z``,
+    from ``h0`` [S, D] when given, over packed sequences when ``cu_seqlens`` is.  Returns ``(out,
+    last_state)``; steps outside every packed sequence are not written."""
+    if out is None or (last_state is None and return_last_state):
+        with _allocating_on(stream, x.device):
+            if out is None:
+                out = torch.empty_like(x, memory_format=torch.contiguous_format)
+            if last_state is None and return_last_state:
+                seqs = x.shape[0] if cu_seqlens is None else cu_seqlens.shape[0] - 1
+                last_state = torch.empty(seqs, x.shape[1], device=x.device, dtype=torch.float32)
+    mssm_gated_scan_fwd(x, r, i, lam, r_bias, i_bias, z, out, last_state, c, h0, cu_seqlens, stream)
+    return out, last_state
+
+
+def gated_scan_bwd(x, r, i, lam, r_bias=None, i_bias=None, z=None, dout=None, c=8.0, h0=None, cu_seqlens=None,
+                   dlast_state=None, stream=None) -> dict:
+    """Allocate the gradients with torch and run the gated recurrence's backward pass: ``dx, dr, di, dz,
+    dlam, dr_bias, di_bias, dh0`` (None where the input is; ``dh0`` is given with ``h0``).  Gradients at steps
+    outside every packed sequence are not written."""
+    device, f32 = x.device, torch.float32
+    batch, dim = x.shape[0], x.shape[1]
+    with _allocating_on(stream, device):
+        def new():
+            return torch.empty_like(x, memory_format=torch.contiguous_format)
+
+        g = dict(dx=new(), dr=new(), di=new(), dz=None if z is None else new(),
+                 dlam=torch.empty(dim, device=device, dtype=f32),
+                 dr_bias=None if r_bias is None else torch.empty(dim, device=device, dtype=f32),
+                 di_bias=None if i_bias is None else torch.empty(dim, device=device, dtype=f32),
+                 dh0=None if h0 is None else torch.empty(h0.shape, device=device, dtype=f32))
+        ws = torch.empty(3, batch, dim, device=device, dtype=f32) if batch > 1 else None
+    mssm_gated_scan_bwd(x, r, i, lam, r_bias, i_bias, z, dout, dlast_state, g["dx"], g["dr"], g["di"], g["dz"],
+                        g["dlam"], g["dr_bias"], g["di_bias"], g["dh0"], ws, c, h0, cu_seqlens, stream)
+    return g
+
+
+def gated_state_update(state, x, r, i, lam, r_bias=None, i_bias=None, z=None, c=8.0, out=None,
+                       stream=None) -> torch.Tensor:
+    """One decode step of the gated recurrence on ``x`` [Bt, D] (``state`` [Bt, D] updated in place);
+    returns ``out``."""
+    if out is None:
+        with _allocating_on(stream, x.device):
+            out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    mssm_gated_state_update(state, x, r, i, lam, r_bias, i_bias, z, out, c, stream)
+    return out
+
+
+class W4Weight:
+    """A weight of 4-bit codes with group scales, laid out for ``w4_linear`` by ``w4_pack``."""
+
+    __slots__ = ("qweight", "qscales", "qzeros", "in_features", "out_features", "group_size")
+
+    def __init__(self, qweight, qscales, qzeros, in_features, out_features, group_size):
+        self.qweight, self.qscales, self.qzeros = qweight, qscales, qzeros
+        self.in_features, self.out_features, self.group_size = in_features, out_features, group_size
+
+
+def w4_pack(codes, scales, zeros=None, in_features=None, group_size=128, stream=None) -> W4Weight:
+    """Lay out a weight of 4-bit codes: ``codes`` [N, (K + 1) / 2] uint8 (input 2j in the low nibble of byte j,
+    2j + 1 in the high one), ``scales`` [N, G] fp32 or bf16 with G = ceil(K / group_size), ``zeros`` [N, G] uint8
+    (None: 8).  ``in_features`` is K, needed when it is odd (default: two per byte)."""
+    if codes.dim() != 2:
+        raise ValueError("codes: expected 2 dims [N, (K + 1) / 2]")
+    n, k = codes.shape[0], int(2 * codes.shape[1] if in_features is None else in_features)
+    words, groups = ctypes.c_int64(), ctypes.c_int64()
+    _check(_lib.mssm_w4_packed_sizes(n, k, group_size, ctypes.byref(words), ctypes.byref(groups)))
+    with _allocating_on(stream, codes.device):
+        q = torch.empty(words.value, device=codes.device, dtype=torch.int32)
+        qs = torch.empty(groups.value, device=codes.device, dtype=scales.dtype)
+        qz = None if zeros is None else torch.empty(groups.value, device=codes.device, dtype=torch.uint8)
+    mssm_w4_pack(codes, scales, zeros, k, group_size, q, qs, qz, stream)
+    return W4Weight(q, qs, qz, k, n, group_size)
+
+
+def w4_linear(x, weight: W4Weight, bias=None, out=None, stream=None) -> torch.Tensor:
+    """``x`` [M, K] times the packed weight's transpose, plus ``bias`` [N]; returns ``out`` [M, N]."""
+    if x.dim() != 2 or x.shape[1] != weight.in_features:
+        raise ValueError(f"x: expected [M, {weight.in_features}], got {list(x.shape)}")
+    if out is None:
+        with _allocating_on(stream, x.device):
+            out = torch.empty(x.shape[0], weight.out_features, device=x.device, dtype=x.dtype)
+    elif out.shape != (x.shape[0], weight.out_features):
+        raise ValueError(f"out: expected [{x.shape[0]}, {weight.out_features}], got {list(out.shape)}")
+    mssm_w4_linear(x, weight.qweight, weight.qscales, weight.qzeros, weight.group_size, bias, out, stream)
     return out

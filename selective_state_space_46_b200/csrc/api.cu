@@ -42,7 +42,7 @@ int g_decode_path = 0;  // MSSM_OPT_DECODE_PATH
 int g_test_hooks = 0;   // MSSM_OPT_TEST_HOOKS  // -1 automatic, else the forced LaunchShape mode
 
 // ---- launch accounting and optional per-kernel event timing (diagnostics)
-int64_t g_launches[MSSM_KERNEL_KINDS] = {};
+int64_t g_launches[MSSM_KERNEL_KINDS_ALL] = {};
 int g_timing = 0;
 struct TimedLaunch {
   int kind;
@@ -50,8 +50,8 @@ struct TimedLaunch {
 };
 std::vector<TimedLaunch> g_pending;
 std::vector<cudaEvent_t> g_event_pool;
-double g_time_ms[MSSM_KERNEL_KINDS] = {};
-int64_t g_timed[MSSM_KERNEL_KINDS] = {};
+double g_time_ms[MSSM_KERNEL_KINDS_ALL] = {};
+int64_t g_timed[MSSM_KERNEL_KINDS_ALL] = {};
 
 cudaEvent_t take_event() {
   if (!g_event_pool.empty()) {
@@ -105,10 +105,10 @@ DeviceState* device_state(int dev) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-size_t esize(int dtype) { return dtype == MSSM_BF16 ? 2 : 4; }  // f32, i32: 4
+size_t esize(int dtype) { return dtype == MSSM_BF16 ? 2 : dtype == MSSM_U8 ? 1 : 4; }  // f32, i32: 4
 
 const char* dname(int dtype) {
-  return dtype == MSSM_BF16 ? "bf16" : dtype == MSSM_F32 ? "f32" : dtype == MSSM_I32 ? "i32" : "?";
+  return dtype == MSSM_BF16 ? "bf16" : dtype == MSSM_F32 ? "f32" : dtype == MSSM_I32 ? "i32" : dtype == MSSM_U8 ? "u8" : "?";
 }
 
 // Shape/dtype check of one tensor.  shape entries < 0 are not checked.
@@ -1133,6 +1133,395 @@ mssm_status mssm_causal_conv1d_update(mssm_tensor* conv_state, const mssm_tensor
   return MSSM_OK;
 }
 
+// ---------------------------------------------------------------------------
+// Gated linear recurrence and 4-bit linear map
+// ---------------------------------------------------------------------------
+}  // extern "C"
+
+namespace {
+
+bool dense(const mssm_tensor* t) {
+  int64_t want = 1;
+  for (int i = t->ndim - 1; i >= 0; --i) {
+    if (t->shape[i] > 1 && t->stride[i] != want) return false;
+    want *= t->shape[i];
+  }
+  return true;
+}
+
+int64_t numel(const mssm_tensor* t) {
+  int64_t n = 1;
+  for (int i = 0; i < t->ndim; ++i) n *= t->shape[i];
+  return n;
+}
+
+// The same start, or dense tensors whose bytes meet.
+bool overlap(const mssm_tensor* a, const mssm_tensor* b) {
+  if (!a || !b || !a->data || !b->data || numel(a) == 0 || numel(b) == 0) return false;
+  if (a->data == b->data) return true;
+  if (!dense(a) || !dense(b)) return false;
+  const char *pa = static_cast<const char*>(a->data), *pb = static_cast<const char*>(b->data);
+  return pa < pb + numel(b) * int64_t(esize(b->dtype)) && pb < pa + numel(a) * int64_t(esize(a->dtype));
+}
+
+// Outputs name every element once and meet neither an input nor one another.
+mssm_status check_outputs(const mssm_tensor* const* outs, const char* const* names, int n,
+                          const mssm_tensor* const* ins, int m) {
+  for (int o = 0; o < n; ++o) {
+    if (!outs[o] || numel(outs[o]) == 0) continue;
+    for (int d = 0; d < outs[o]->ndim; ++d)
+      if (outs[o]->shape[d] > 1 && outs[o]->stride[d] == 0)
+        return fail(MSSM_ERR_INVALID_ARG, "%s: an output must not be broadcast (stride 0 in dim %d)", names[o], d);
+    for (int k = 0; k < m; ++k)
+      if (overlap(outs[o], ins[k])) return fail(MSSM_ERR_INVALID_ARG, "%s must not alias an input", names[o]);
+    for (int k = 0; k < o; ++k)
+      if (overlap(outs[o], outs[k])) return fail(MSSM_ERR_INVALID_ARG, "%s must not alias %s", names[o], names[k]);
+  }
+  return MSSM_OK;
+}
+
+mssm_status check_scale(float c) {
+  if (!(c > 0.0f) || c > 3.0e38f) return fail(MSSM_ERR_INVALID_ARG, "decay_scale must be positive and finite");
+  return MSSM_OK;
+}
+
+// The inputs shared by the forward and backward scans.
+struct GatedCall {
+  mssm::GatedArgs a{};
+  int dtype = 0;
+  int64_t Bt = 0, D = 0, L = 0, S = 0;
+};
+
+mssm_status gated_prepare(const mssm_tensor* x, const mssm_tensor* r, const mssm_tensor* i, const mssm_tensor* lam,
+                          const mssm_tensor* r_bias, const mssm_tensor* i_bias, const mssm_tensor* z,
+                          const mssm_gated_ext* ext, GatedCall& call) {
+  if (!x) return fail(MSSM_ERR_INVALID_ARG, "x: null tensor descriptor");
+  if (x->ndim != 3) return fail(MSSM_ERR_INVALID_ARG, "x: expected 3 dims [Bt, D, L]");
+  const int dt = x->dtype;
+  if (dt != MSSM_F32 && dt != MSSM_BF16) return fail(MSSM_ERR_INVALID_ARG, "x: dtype must be f32 or bf16");
+  if (ext && ext->struct_size < int32_t(sizeof(mssm_gated_ext)))
+    return fail(MSSM_ERR_INVALID_ARG, "ext->struct_size = %d; expected at least %d", int(ext->struct_size),
+                int(sizeof(mssm_gated_ext)));
+  const float c = ext ? ext->decay_scale : 8.0f;
+  const int64_t Bt = x->shape[0], Dd = x->shape[1], L = x->shape[2];
+  const int64_t s_bdl[3] = {Bt, Dd, L}, s_d[1] = {Dd}, any[1] = {-1};
+  mssm_status st;
+  if ((st = check_scale(c)) != MSSM_OK) return st;
+  if ((st = check(x, "x", 3, s_bdl, dt, true)) != MSSM_OK) return st;
+  if ((st = check(r, "r", 3, s_bdl, dt, true)) != MSSM_OK) return st;
+  if ((st = check(i, "i", 3, s_bdl, dt, true)) != MSSM_OK) return st;
+  if ((st = check(lam, "lam", 1, s_d, MSSM_F32, false)) != MSSM_OK) return st;
+  if (r_bias && (st = check(r_bias, "r_bias", 1, s_d, MSSM_F32, false)) != MSSM_OK) return st;
+  if (i_bias && (st = check(i_bias, "i_bias", 1, s_d, MSSM_F32, false)) != MSSM_OK) return st;
+  if (z && (st = check(z, "z", 3, s_bdl, dt, true)) != MSSM_OK) return st;
+  const mssm_tensor* cu = ext ? ext->cu_seqlens : nullptr;
+  const mssm_tensor* h0 = ext ? ext->h0 : nullptr;
+  int64_t S = Bt;
+  if (cu) {
+    if ((st = check(cu, "cu_seqlens", 1, any, MSSM_I32, true)) != MSSM_OK) return st;
+    if (cu->shape[0] < 1) return fail(MSSM_ERR_INVALID_ARG, "cu_seqlens: expected S + 1 >= 1 offsets");
+    if (Bt != 1)
+      return fail(MSSM_ERR_INVALID_ARG, "with cu_seqlens, x/r/i/z/out must be [1, D, T] (got Bt = %lld)",
+                  (long long)Bt);
+    S = cu->shape[0] - 1;
+  }
+  if (Bt > INT32_MAX || Dd > INT32_MAX || L > INT32_MAX - (1 << 16) || S > INT32_MAX - 2)
+    return fail(MSSM_ERR_UNSUPPORTED, "Bt, D, L and the sequence count must each fit in 31 bits");
+  if (Bt * Dd > int64_t(INT32_MAX) || S * Dd > int64_t(INT32_MAX))
+    return fail(MSSM_ERR_UNSUPPORTED, "Bt * D (or the sequence count * D) must fit in 31 bits");
+  const int64_t s_sd[2] = {S, Dd};
+  if (h0 && (st = check(h0, "h0", 2, s_sd, MSSM_F32, false)) != MSSM_OK) return st;
+
+  mssm::GatedArgs& a = call.a;
+  a.x = x->data; a.r = r->data; a.i = i->data; a.z = z ? z->data : nullptr;
+  a.x_sb = x->stride[0]; a.x_sd = x->stride[1]; a.r_sb = r->stride[0]; a.r_sd = r->stride[1];
+  a.i_sb = i->stride[0]; a.i_sd = i->stride[1];
+  a.z_sb = z ? z->stride[0] : 0; a.z_sd = z ? z->stride[1] : 0;
+  a.lam = static_cast<const float*>(lam->data); a.lam_s = lam->stride[0];
+  a.rb = r_bias ? static_cast<const float*>(r_bias->data) : nullptr; a.rb_s = r_bias ? r_bias->stride[0] : 0;
+  a.ib = i_bias ? static_cast<const float*>(i_bias->data) : nullptr; a.ib_s = i_bias ? i_bias->stride[0] : 0;
+  a.c = c;
+  a.h0 = h0 ? static_cast<const float*>(h0->data) : nullptr;
+  a.h0_sb = h0 ? h0->stride[0] : 0; a.h0_sd = h0 ? h0->stride[1] : 0;
+  a.cu = cu ? static_cast<const int*>(cu->data) : nullptr;
+  a.S = int(S); a.Bt = int(Bt); a.D = int(Dd); a.L = int(L);
+  call.dtype = dt;
+  call.Bt = Bt; call.D = Dd; call.L = L; call.S = S;
+  return MSSM_OK;
+}
+
+// Warps per row of the gated scans: rows that fill the GPU one warp each need no barriers; fewer rows
+// of more than one warp's tile take a CTA each.
+int gated_warps(int64_t rows, int64_t L) {
+  return L > 32 * mssm::kGs && rows < 148 * 12 ? mssm::kGatedWarps : 1;
+}
+
+}  // namespace
+
+extern "C" {
+
+mssm_status mssm_gated_scan_fwd(const mssm_tensor* x, const mssm_tensor* r, const mssm_tensor* i,
+                                const mssm_tensor* lam, const mssm_tensor* r_bias, const mssm_tensor* i_bias,
+                                const mssm_tensor* z, const mssm_gated_ext* ext, mssm_tensor* out,
+                                mssm_tensor* last_state, void* stream) {
+  GatedCall call;
+  mssm_status st = gated_prepare(x, r, i, lam, r_bias, i_bias, z, ext, call);
+  if (st != MSSM_OK) return st;
+  const int64_t s_bdl[3] = {call.Bt, call.D, call.L}, s_sd[2] = {call.S, call.D};
+  if ((st = check(out, "out", 3, s_bdl, call.dtype, true)) != MSSM_OK) return st;
+  if (last_state && (st = check(last_state, "last_state", 2, s_sd, MSSM_F32, false)) != MSSM_OK) return st;
+  const mssm_tensor* ins[] = {x, r, i, lam, r_bias, i_bias, z, ext ? ext->h0 : nullptr, ext ? ext->cu_seqlens : nullptr};
+  const mssm_tensor* outs[] = {out, last_state};
+  const char* names[] = {"out", "last_state"};
+  if ((st = check_outputs(outs, names, 2, ins, 9)) != MSSM_OK) return st;
+  if (call.Bt == 0 || call.D == 0 || call.S == 0) return MSSM_OK;
+  mssm::GatedArgs& a = call.a;
+  a.out = out->data; a.o_sb = out->stride[0]; a.o_sd = out->stride[1];
+  a.last = last_state ? static_cast<float*>(last_state->data) : nullptr;
+  a.ls_sb = last_state ? last_state->stride[0] : 0; a.ls_sd = last_state ? last_state->stride[1] : 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  std::lock_guard<std::mutex> lk(g_mu);
+  cudaError_t e = mssm::device_error_word(&a.err);
+  if (e != cudaSuccess) return cuda_fail(e, "device error word");
+  e = tracked(MSSM_KERNEL_GATED_SCAN, s,
+              [&] { return mssm::launch_gated_scan(a, gated_warps(call.Bt * call.D, call.L), call.dtype, s); });
+  if (e != cudaSuccess) return cuda_fail(e, "gated scan kernel launch");
+  return MSSM_OK;
+}
+
+mssm_status mssm_gated_scan_bwd(const mssm_tensor* x, const mssm_tensor* r, const mssm_tensor* i,
+                                const mssm_tensor* lam, const mssm_tensor* r_bias, const mssm_tensor* i_bias,
+                                const mssm_tensor* z, const mssm_gated_ext* ext, const mssm_tensor* dout,
+                                const mssm_tensor* dlast_state, mssm_tensor* dx, mssm_tensor* dr, mssm_tensor* di,
+                                mssm_tensor* dz, mssm_tensor* dlam, mssm_tensor* dr_bias, mssm_tensor* di_bias,
+                                mssm_tensor* dh0, mssm_tensor* workspace, void* stream) {
+  GatedCall call;
+  mssm_status st = gated_prepare(x, r, i, lam, r_bias, i_bias, z, ext, call);
+  if (st != MSSM_OK) return st;
+  const int dt = call.dtype;
+  const int64_t s_bdl[3] = {call.Bt, call.D, call.L}, s_sd[2] = {call.S, call.D}, s_d[1] = {call.D},
+                s_ws[3] = {3, call.Bt, call.D};
+  if (!z != !dz) return fail(MSSM_ERR_INVALID_ARG, "dz must be given exactly when z is");
+  if (!r_bias != !dr_bias) return fail(MSSM_ERR_INVALID_ARG, "dr_bias must be given exactly when r_bias is");
+  if (!i_bias != !di_bias) return fail(MSSM_ERR_INVALID_ARG, "di_bias must be given exactly when i_bias is");
+  if ((st = check(dout, "dout", 3, s_bdl, dt, true)) != MSSM_OK) return st;
+  if (dlast_state && (st = check(dlast_state, "dlast_state", 2, s_sd, MSSM_F32, false)) != MSSM_OK) return st;
+  if ((st = check(dx, "dx", 3, s_bdl, dt, true)) != MSSM_OK) return st;
+  if ((st = check(dr, "dr", 3, s_bdl, dt, true)) != MSSM_OK) return st;
+  if ((st = check(di, "di", 3, s_bdl, dt, true)) != MSSM_OK) return st;
+  if (dz && (st = check(dz, "dz", 3, s_bdl, dt, true)) != MSSM_OK) return st;
+  if ((st = check(dlam, "dlam", 1, s_d, MSSM_F32, true)) != MSSM_OK) return st;
+  if (dr_bias && (st = check(dr_bias, "dr_bias", 1, s_d, MSSM_F32, true)) != MSSM_OK) return st;
+  if (di_bias && (st = check(di_bias, "di_bias", 1, s_d, MSSM_F32, true)) != MSSM_OK) return st;
+  if (dh0 && (st = check(dh0, "dh0", 2, s_sd, MSSM_F32, false)) != MSSM_OK) return st;
+  if (workspace && (st = check(workspace, "workspace", 3, s_ws, MSSM_F32, true)) != MSSM_OK) return st;
+  if (workspace && !dense(workspace)) return fail(MSSM_ERR_UNSUPPORTED, "workspace must be dense");
+  if (call.Bt > 1 && !workspace) return fail(MSSM_ERR_INVALID_ARG, "workspace: needed when Bt is above 1");
+  if (call.L > (int64_t(1) << 23)) return fail(MSSM_ERR_UNSUPPORTED, "the backward scan takes at most 2^23 steps");
+  const mssm_tensor* ins[] = {x, r, i, lam, r_bias, i_bias, z, ext ? ext->h0 : nullptr,
+                              ext ? ext->cu_seqlens : nullptr, dout, dlast_state};
+  const mssm_tensor* outs[] = {dx, dr, di, dz, dlam, dr_bias, di_bias, dh0, workspace};
+  const char* names[] = {"dx", "dr", "di", "dz", "dlam", "dr_bias", "di_bias", "dh0", "workspace"};
+  if ((st = check_outputs(outs, names, 9, ins, 11)) != MSSM_OK) return st;
+  if (call.D == 0) return MSSM_OK;
+  mssm::GatedArgs& a = call.a;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  std::lock_guard<std::mutex> lk(g_mu);
+  cudaError_t e = cudaSuccess;
+  if (call.Bt == 0 || call.S == 0) {  // no sequence: the parameters' gradients are zero
+    for (mssm_tensor* t : {dlam, dr_bias, di_bias})
+      if (t && e == cudaSuccess) e = cudaMemsetAsync(t->data, 0, size_t(call.D) * 4, s);
+    return e == cudaSuccess ? MSSM_OK : cuda_fail(e, "cudaMemsetAsync(gradients)");
+  }
+  a.dout = dout->data; a.g_sb = dout->stride[0]; a.g_sd = dout->stride[1];
+  a.dlast = dlast_state ? static_cast<const float*>(dlast_state->data) : nullptr;
+  a.dl_sb = dlast_state ? dlast_state->stride[0] : 0; a.dl_sd = dlast_state ? dlast_state->stride[1] : 0;
+  a.dx = dx->data; a.dr = dr->data; a.di = di->data; a.dz = dz ? dz->data : nullptr;
+  a.dx_sb = dx->stride[0]; a.dx_sd = dx->stride[1]; a.dr_sb = dr->stride[0]; a.dr_sd = dr->stride[1];
+  a.di_sb = di->stride[0]; a.di_sd = di->stride[1];
+  a.dz_sb = dz ? dz->stride[0] : 0; a.dz_sd = dz ? dz->stride[1] : 0;
+  a.dh0 = dh0 ? static_cast<float*>(dh0->data) : nullptr;
+  a.dh_sb = dh0 ? dh0->stride[0] : 0; a.dh_sd = dh0 ? dh0->stride[1] : 0;
+  a.dlam = static_cast<float*>(dlam->data);
+  a.drb = dr_bias ? static_cast<float*>(dr_bias->data) : nullptr;
+  a.dib = di_bias ? static_cast<float*>(di_bias->data) : nullptr;
+  a.part = call.Bt > 1 ? static_cast<float*>(workspace->data) : nullptr;
+  e = mssm::device_error_word(&a.err);
+  if (e != cudaSuccess) return cuda_fail(e, "device error word");
+  int warps = gated_warps(call.Bt * call.D, call.L);
+  if (call.L > (1 << 19)) warps = mssm::kGatedWarps;  // the checkpoints of four rows share 48 KB
+  const int64_t tile = 32 * warps * mssm::kGs;
+  a.ntiles = int((call.L + mssm::kGs + tile - 1) / tile);
+  e = tracked(MSSM_KERNEL_GATED_BWD, s, [&] { return mssm::launch_gated_bwd(a, warps, call.dtype, s); });
+  if (e != cudaSuccess) return cuda_fail(e, "gated backward kernel launch");
+  return MSSM_OK;
+}
+
+mssm_status mssm_gated_state_update(mssm_tensor* state, const mssm_tensor* x, const mssm_tensor* r,
+                                    const mssm_tensor* i, const mssm_tensor* lam, const mssm_tensor* r_bias,
+                                    const mssm_tensor* i_bias, const mssm_tensor* z, float decay_scale,
+                                    mssm_tensor* out, void* stream) {
+  if (!x) return fail(MSSM_ERR_INVALID_ARG, "x: null tensor descriptor");
+  if (x->ndim != 2) return fail(MSSM_ERR_INVALID_ARG, "x: expected 2 dims [Bt, D]");
+  const int dt = x->dtype;
+  if (dt != MSSM_F32 && dt != MSSM_BF16) return fail(MSSM_ERR_INVALID_ARG, "x: dtype must be f32 or bf16");
+  const int64_t Bt = x->shape[0], Dd = x->shape[1], s_bd[2] = {Bt, Dd}, s_d[1] = {Dd};
+  mssm_status st;
+  if ((st = check_scale(decay_scale)) != MSSM_OK) return st;
+  if ((st = check(state, "state", 2, s_bd, MSSM_F32, false)) != MSSM_OK) return st;
+  if ((st = check(x, "x", 2, s_bd, dt, false)) != MSSM_OK) return st;
+  if ((st = check(r, "r", 2, s_bd, dt, false)) != MSSM_OK) return st;
+  if ((st = check(i, "i", 2, s_bd, dt, false)) != MSSM_OK) return st;
+  if ((st = check(lam, "lam", 1, s_d, MSSM_F32, false)) != MSSM_OK) return st;
+  if (r_bias && (st = check(r_bias, "r_bias", 1, s_d, MSSM_F32, false)) != MSSM_OK) return st;
+  if (i_bias && (st = check(i_bias, "i_bias", 1, s_d, MSSM_F32, false)) != MSSM_OK) return st;
+  if (z && (st = check(z, "z", 2, s_bd, dt, false)) != MSSM_OK) return st;
+  if ((st = check(out, "out", 2, s_bd, dt, false)) != MSSM_OK) return st;
+  if (Bt > INT32_MAX || Dd > INT32_MAX) return fail(MSSM_ERR_UNSUPPORTED, "Bt and D must fit in 31 bits");
+  if (Bt * Dd > int64_t(INT32_MAX)) return fail(MSSM_ERR_UNSUPPORTED, "Bt * D must fit in 31 bits");
+  const mssm_tensor* ins[] = {x, r, i, lam, r_bias, i_bias, z};
+  const mssm_tensor* outs[] = {out, state};
+  const char* names[] = {"out", "state"};
+  if ((st = check_outputs(outs, names, 2, ins, 7)) != MSSM_OK) return st;
+  if (Bt == 0 || Dd == 0) return MSSM_OK;
+  mssm::GatedStepArgs a{};
+  a.state = static_cast<float*>(state->data); a.st_sb = state->stride[0]; a.st_sd = state->stride[1];
+  a.x = x->data; a.r = r->data; a.i = i->data; a.z = z ? z->data : nullptr; a.out = out->data;
+  a.x_sb = x->stride[0]; a.x_sd = x->stride[1]; a.r_sb = r->stride[0]; a.r_sd = r->stride[1];
+  a.i_sb = i->stride[0]; a.i_sd = i->stride[1];
+  a.z_sb = z ? z->stride[0] : 0; a.z_sd = z ? z->stride[1] : 0;
+  a.o_sb = out->stride[0]; a.o_sd = out->stride[1];
+  a.lam = static_cast<const float*>(lam->data); a.lam_s = lam->stride[0];
+  a.rb = r_bias ? static_cast<const float*>(r_bias->data) : nullptr; a.rb_s = r_bias ? r_bias->stride[0] : 0;
+  a.ib = i_bias ? static_cast<const float*>(i_bias->data) : nullptr; a.ib_s = i_bias ? i_bias->stride[0] : 0;
+  a.c = decay_scale;
+  a.Bt = int(Bt); a.D = int(Dd);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  std::lock_guard<std::mutex> lk(g_mu);
+  cudaError_t e = tracked(MSSM_KERNEL_GATED_STEP, s, [&] { return mssm::launch_gated_step(a, dt, s); });
+  if (e != cudaSuccess) return cuda_fail(e, "gated state update launch");
+  return MSSM_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+struct W4Shape {
+  int64_t tiles, blocks, groups;  // tiles of 16 outputs, blocks of 64 inputs, groups stored per tile
+};
+
+mssm_status w4_shape(int64_t N, int64_t K, int64_t group, W4Shape& w) {
+  if (N < 1 || K < 1) return fail(MSSM_ERR_INVALID_ARG, "N and K must be at least 1");
+  if (group < 32 || group % 32 != 0)
+    return fail(MSSM_ERR_UNSUPPORTED, "group = %lld; must be a positive multiple of 32", (long long)group);
+  const int64_t most = INT32_MAX - 64;
+  if (N > most || K > most || group > most) return fail(MSSM_ERR_UNSUPPORTED, "N, K and group must be below 2^31 - 64");
+  w.tiles = (N + mssm::kW4Rows - 1) / mssm::kW4Rows;
+  w.blocks = (K + mssm::kW4K - 1) / mssm::kW4K;
+  w.groups = (w.blocks * mssm::kW4K + group - 1) / group;
+  return MSSM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+mssm_status mssm_w4_packed_sizes(int64_t N, int64_t K, int64_t group, int64_t* qweight, int64_t* qscales) {
+  W4Shape w;
+  mssm_status st = w4_shape(N, K, group, w);
+  if (st != MSSM_OK) return st;
+  if (qweight) *qweight = w.tiles * w.blocks * 128;
+  if (qscales) *qscales = w.tiles * w.groups * mssm::kW4Rows;
+  return MSSM_OK;
+}
+
+mssm_status mssm_w4_pack(const mssm_tensor* codes, const mssm_tensor* scales, const mssm_tensor* zeros, int64_t K,
+                         int64_t group, mssm_tensor* qweight, mssm_tensor* qscales, mssm_tensor* qzeros,
+                         void* stream) {
+  if (!codes || codes->ndim != 2) return fail(MSSM_ERR_INVALID_ARG, "codes: expected 2 dims [N, (K + 1) / 2]");
+  const int64_t N = codes->shape[0];
+  W4Shape w;
+  mssm_status st = w4_shape(N, K, group, w);
+  if (st != MSSM_OK) return st;
+  const int64_t G = (K + group - 1) / group;
+  if (!scales || (scales->dtype != MSSM_F32 && scales->dtype != MSSM_BF16))
+    return fail(MSSM_ERR_INVALID_ARG, "scales: dtype must be f32 or bf16");
+  const int64_t s_nk[2] = {N, (K + 1) / 2}, s_ng[2] = {N, G}, s_q[1] = {w.tiles * w.blocks * 128},
+                s_s[1] = {w.tiles * w.groups * mssm::kW4Rows};
+  if ((st = check(codes, "codes", 2, s_nk, MSSM_U8, false)) != MSSM_OK) return st;
+  if ((st = check(scales, "scales", 2, s_ng, scales->dtype, false)) != MSSM_OK) return st;
+  if (zeros && (st = check(zeros, "zeros", 2, s_ng, MSSM_U8, false)) != MSSM_OK) return st;
+  if (!zeros != !qzeros) return fail(MSSM_ERR_INVALID_ARG, "qzeros must be given exactly when zeros is");
+  if ((st = check(qweight, "qweight", 1, s_q, MSSM_I32, true)) != MSSM_OK) return st;
+  if ((st = check(qscales, "qscales", 1, s_s, scales->dtype, true)) != MSSM_OK) return st;
+  if (qzeros && (st = check(qzeros, "qzeros", 1, s_s, MSSM_U8, true)) != MSSM_OK) return st;
+  const mssm_tensor* ins[] = {codes, scales, zeros};
+  const mssm_tensor* outs[] = {qweight, qscales, qzeros};
+  const char* names[] = {"qweight", "qscales", "qzeros"};
+  if ((st = check_outputs(outs, names, 3, ins, 3)) != MSSM_OK) return st;
+  mssm::W4PackArgs a{};
+  a.codes = static_cast<const uint8_t*>(codes->data); a.c_sn = codes->stride[0]; a.c_sk = codes->stride[1];
+  a.scale = scales->data; a.s_sn = scales->stride[0]; a.s_sg = scales->stride[1];
+  a.zero = zeros ? static_cast<const uint8_t*>(zeros->data) : nullptr;
+  a.z_sn = zeros ? zeros->stride[0] : 0; a.z_sg = zeros ? zeros->stride[1] : 0;
+  a.q = static_cast<uint32_t*>(qweight->data); a.q_scale = qscales->data;
+  a.q_zero = qzeros ? static_cast<uint8_t*>(qzeros->data) : nullptr;
+  a.N = int(N); a.K = int(K); a.G = int(G); a.group = int(group);
+  a.tiles = int(w.tiles); a.blocks = int(w.blocks); a.groups = int(w.groups);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  std::lock_guard<std::mutex> lk(g_mu);
+  cudaError_t e = tracked(MSSM_KERNEL_W4_LINEAR, s, [&] { return mssm::launch_w4_pack(a, scales->dtype, s); });
+  if (e != cudaSuccess) return cuda_fail(e, "4-bit weight layout launch");
+  return MSSM_OK;
+}
+
+mssm_status mssm_w4_linear(const mssm_tensor* x, const mssm_tensor* qweight, const mssm_tensor* qscales,
+                           const mssm_tensor* qzeros, int64_t group, const mssm_tensor* bias, mssm_tensor* out,
+                           void* stream) {
+  if (!x || x->ndim != 2) return fail(MSSM_ERR_INVALID_ARG, "x: expected 2 dims [M, K]");
+  if (!out || out->ndim != 2) return fail(MSSM_ERR_INVALID_ARG, "out: expected 2 dims [M, N]");
+  const int dt = x->dtype;
+  if (dt != MSSM_F32 && dt != MSSM_BF16) return fail(MSSM_ERR_INVALID_ARG, "x: dtype must be f32 or bf16");
+  const int64_t M = x->shape[0], K = x->shape[1], N = out->shape[1];
+  W4Shape w;
+  mssm_status st = w4_shape(N, K, group, w);
+  if (st != MSSM_OK) return st;
+  if (!qscales || (qscales->dtype != MSSM_F32 && qscales->dtype != MSSM_BF16))
+    return fail(MSSM_ERR_INVALID_ARG, "qscales: dtype must be f32 or bf16");
+  const int64_t s_mk[2] = {M, K}, s_mn[2] = {M, N}, s_n[1] = {N}, s_q[1] = {w.tiles * w.blocks * 128},
+                s_s[1] = {w.tiles * w.groups * mssm::kW4Rows};
+  if ((st = check(x, "x", 2, s_mk, dt, true)) != MSSM_OK) return st;
+  if ((st = check(qweight, "qweight", 1, s_q, MSSM_I32, true)) != MSSM_OK) return st;
+  if ((st = check(qscales, "qscales", 1, s_s, qscales->dtype, true)) != MSSM_OK) return st;
+  if (qzeros && (st = check(qzeros, "qzeros", 1, s_s, MSSM_U8, true)) != MSSM_OK) return st;
+  if (bias && (st = check(bias, "bias", 1, s_n, MSSM_F32, false)) != MSSM_OK) return st;
+  if ((st = check(out, "out", 2, s_mn, dt, false)) != MSSM_OK) return st;
+  if (!aligned16(qweight->data) || !aligned16(qscales->data) || (qzeros && !aligned16(qzeros->data)))
+    return fail(MSSM_ERR_UNSUPPORTED, "qweight, qscales and qzeros must be 16-byte aligned");
+  if (M > 65535 * 8) return fail(MSSM_ERR_UNSUPPORTED, "M = %lld tokens; at most %d", (long long)M, 65535 * 8);
+  const mssm_tensor* ins[] = {x, qweight, qscales, qzeros, bias};
+  const mssm_tensor* outs[] = {out};
+  const char* names[] = {"out"};
+  if ((st = check_outputs(outs, names, 1, ins, 5)) != MSSM_OK) return st;
+  if (M == 0) return MSSM_OK;
+  mssm::W4Args a{};
+  a.x = x->data; a.x_sm = x->stride[0];
+  a.q = static_cast<const uint4*>(qweight->data);
+  a.scale = qscales->data;
+  a.zero = qzeros ? static_cast<const uint8_t*>(qzeros->data) : nullptr;
+  a.bias = bias ? static_cast<const float*>(bias->data) : nullptr; a.bias_s = bias ? bias->stride[0] : 0;
+  a.out = out->data; a.o_sm = out->stride[0]; a.o_sn = out->stride[1];
+  a.M = int(M); a.N = int(N); a.K = int(K);
+  a.blocks = int(w.blocks); a.groups = int(w.groups); a.group = int(group);
+  a.vec_x = aligned16(x->data) && (M == 1 || (x->stride[0] * int64_t(esize(dt))) % 16 == 0);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  std::lock_guard<std::mutex> lk(g_mu);
+  cudaError_t e = tracked(MSSM_KERNEL_W4_LINEAR, s, [&] { return mssm::launch_w4_linear(a, dt, qscales->dtype, s); });
+  if (e != cudaSuccess) return cuda_fail(e, "4-bit linear launch");
+  return MSSM_OK;
+}
+
 mssm_status mssm_scan_plan(int64_t Bt, int64_t D, int64_t L, int sm_count, int* rows_per_cta,
                            int64_t* chunk_len, int64_t* n_chunks, int* schedule) {
   return mssm_scan_plan_packed(Bt, D, L, -1, sm_count, rows_per_cta, chunk_len, n_chunks, schedule);
@@ -1189,6 +1578,12 @@ mssm_status mssm_scan_plan_query(int64_t S, int64_t D, int64_t max_seqlen, int64
 
 mssm_status mssm_kernel_stats(int64_t launches[MSSM_KERNEL_KINDS], int64_t timed[MSSM_KERNEL_KINDS],
                               double ms[MSSM_KERNEL_KINDS], int reset) {
+  return mssm_kernel_stats_all(MSSM_KERNEL_KINDS, launches, timed, ms, reset);
+}
+
+mssm_status mssm_kernel_stats_all(int kinds, int64_t* launches, int64_t* timed, double* ms, int reset) {
+  if (kinds < 0 || kinds > MSSM_KERNEL_KINDS_ALL)
+    return fail(MSSM_ERR_INVALID_ARG, "kinds = %d must lie in [0, %d]", kinds, int(MSSM_KERNEL_KINDS_ALL));
   std::lock_guard<std::mutex> lk(g_mu);
   mssm_status st = MSSM_OK;
   for (const TimedLaunch& t : g_pending) {
@@ -1205,10 +1600,10 @@ mssm_status mssm_kernel_stats(int64_t launches[MSSM_KERNEL_KINDS], int64_t timed
     g_event_pool.push_back(t.b);
   }
   g_pending.clear();
-  for (int k = 0; k < MSSM_KERNEL_KINDS; ++k) {
-    if (launches) launches[k] = g_launches[k];
-    if (timed) timed[k] = g_timed[k];
-    if (ms) ms[k] = g_time_ms[k];
+  for (int k = 0; k < MSSM_KERNEL_KINDS_ALL; ++k) {
+    if (launches && k < kinds) launches[k] = g_launches[k];
+    if (timed && k < kinds) timed[k] = g_timed[k];
+    if (ms && k < kinds) ms[k] = g_time_ms[k];
     if (reset) {
       g_launches[k] = 0;
       g_timed[k] = 0;

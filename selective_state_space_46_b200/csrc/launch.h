@@ -6,7 +6,9 @@
 #include "bwd.cuh"
 #include "conv.cuh"
 #include "decode.cuh"
+#include "gated.cuh"
 #include "scan.cuh"
+#include "w4.cuh"
 
 namespace mssm {
 
@@ -42,6 +44,14 @@ cudaError_t launch_causal_conv1d_update(const ConvUpdateArgs& a, int dtype, cuda
 // Backward scan: pass A (chunk summaries both ways and their folds, when there is more than
 // one chunk) and pass B (recompute and backward sweep per chunk).
 cudaError_t launch_scan_bwd(const BwdArgs& a, int dtype, bool has_z, cudaStream_t s);
+// Gated linear recurrence: `warps` (1 or kGatedWarps) warps per row.  The backward pass is followed by the
+// sum of the batch's row sums when a.part is given.
+cudaError_t launch_gated_scan(const GatedArgs& a, int warps, int dtype, cudaStream_t s);
+cudaError_t launch_gated_bwd(const GatedArgs& a, int warps, int dtype, cudaStream_t s);
+cudaError_t launch_gated_step(const GatedStepArgs& a, int dtype, cudaStream_t s);
+// 4-bit linear map: the layout of a weight, and the product.
+cudaError_t launch_w4_pack(const W4PackArgs& a, int scale_dtype, cudaStream_t s);
+cudaError_t launch_w4_linear(const W4Args& a, int dtype, int scale_dtype, cudaStream_t s);
 // Reads (and optionally clears) the current device's error word.
 cudaError_t read_device_error(unsigned int* value, bool clear);
 
