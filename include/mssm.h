@@ -466,6 +466,10 @@ mssm_status mssm_get_error(void *stream);
  *     the first gives up its bounded wait (about 0.5 s), runs from a zero state
  *     and sets the device error word; mssm_get_error then reports
  *     MSSM_ERR_TIMEOUT.  No fault, trap or unbounded wait is involved.
+ *   MSSM_OPT_GATED_WARPS (value 0, 1, 4 or 8): warps of a CTA that share a row of the
+ *     gated scans; 0 automatic.
+ *   MSSM_OPT_GATED_SPLIT (value 0, 1, 2, 4 or 8): CTAs (a cluster, of 8 warps each) that
+ *     share a row of the gated scans; 0 automatic.
  * Unknown options or invalid values return MSSM_ERR_INVALID_ARG.
  */
 typedef enum {
@@ -476,7 +480,9 @@ typedef enum {
     MSSM_OPT_DECODE_PATH = 5,
     MSSM_OPT_TEST_HOOKS = 6,
     MSSM_OPT_ROWS_PER_CTA = 7,
-    MSSM_OPT_ROWS_PER_THREAD = 8
+    MSSM_OPT_ROWS_PER_THREAD = 8,
+    MSSM_OPT_GATED_WARPS = 9,
+    MSSM_OPT_GATED_SPLIT = 10
 } mssm_option;
 mssm_status mssm_set_option(int option, int64_t value);
 

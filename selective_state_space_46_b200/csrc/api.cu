@@ -39,6 +39,8 @@ int g_schedule = -1;
 int g_rows_per_cta = 0;     // 0 automatic, else 32, 64 or 128
 int g_rows_per_thread = 0;  // 0 automatic, else 1 or 2
 int g_decode_path = 0;  // MSSM_OPT_DECODE_PATH
+int g_gated_warps = 0;  // MSSM_OPT_GATED_WARPS
+int g_gated_split = 0;  // MSSM_OPT_GATED_SPLIT
 int g_test_hooks = 0;   // MSSM_OPT_TEST_HOOKS  // -1 automatic, else the forced LaunchShape mode
 
 // ---- launch accounting and optional per-kernel event timing (diagnostics)
@@ -377,6 +379,16 @@ mssm_status mssm_set_option(int option, int64_t value) {
     case MSSM_OPT_DECODE_PATH:
       if (value < 0 || value > 3) return fail(MSSM_ERR_INVALID_ARG, "DECODE_PATH takes 0 (automatic) to 3");
       g_decode_path = int(value);
+      return MSSM_OK;
+    case MSSM_OPT_GATED_WARPS:
+      if (value != 0 && value != 1 && value != 4 && value != 8)
+        return fail(MSSM_ERR_INVALID_ARG, "GATED_WARPS takes 0, 1, 4 or 8");
+      g_gated_warps = int(value);
+      return MSSM_OK;
+    case MSSM_OPT_GATED_SPLIT:
+      if (value != 0 && value != 1 && value != 2 && value != 4 && value != 8)
+        return fail(MSSM_ERR_INVALID_ARG, "GATED_SPLIT takes 0, 1, 2, 4 or 8");
+      g_gated_split = int(value);
       return MSSM_OK;
     case MSSM_OPT_KERNEL_TIMING:
       if (value != 0 && value != 1) return fail(MSSM_ERR_INVALID_ARG, "KERNEL_TIMING takes 0 or 1");
@@ -1250,10 +1262,22 @@ mssm_status gated_prepare(const mssm_tensor* x, const mssm_tensor* r, const mssm
   return MSSM_OK;
 }
 
-// Warps per row of the gated scans: rows that fill the GPU one warp each need no barriers; fewer rows
-// of more than one warp's tile take a CTA each.
-int gated_warps(int64_t rows, int64_t L) {
-  return L > 32 * mssm::kGs && rows < 148 * 12 ? mssm::kGatedWarps : 1;
+// Warps of a CTA and CTAs that share a row of the gated scans.  Rows that fill the GPU with one warp each
+// need no barriers; fewer rows take 4 or 8 warps, and still fewer the CTAs of a cluster, as far as the
+// length gives each its steps.
+struct GatedShape {
+  int warps, split;
+};
+
+GatedShape gated_shape(int64_t rows, int64_t L, int sms) {
+  const int64_t want = int64_t(sms) * 24, step = 32 * mssm::kGs;  // warps to fill the GPU, steps of a warp
+  GatedShape g{1, 1};
+  if (L > step && rows < want) g.warps = L > 4 * step && rows * 4 < want ? 8 : 4;
+  while (g.warps == 8 && g.split < mssm::kMaxSplit && rows * 8 * g.split < want && L > 8 * step * g.split) g.split *= 2;
+  if (g_gated_warps) g.warps = g_gated_warps, g.split = 1;
+  if (g_gated_split) g.split = g_gated_split;
+  if (g.split > 1) g.warps = 8;
+  return g;
 }
 
 }  // namespace
@@ -1283,8 +1307,11 @@ mssm_status mssm_gated_scan_fwd(const mssm_tensor* x, const mssm_tensor* r, cons
   std::lock_guard<std::mutex> lk(g_mu);
   cudaError_t e = mssm::device_error_word(&a.err);
   if (e != cudaSuccess) return cuda_fail(e, "device error word");
-  e = tracked(MSSM_KERNEL_GATED_SCAN, s,
-              [&] { return mssm::launch_gated_scan(a, gated_warps(call.Bt * call.D, call.L), call.dtype, s); });
+  int dev = -1;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  const GatedShape g = gated_shape(call.Bt * call.D, call.L, device_state(dev)->sm_count);
+  a.split = g.split;
+  e = tracked(MSSM_KERNEL_GATED_SCAN, s, [&] { return mssm::launch_gated_scan(a, g.warps, call.dtype, s); });
   if (e != cudaSuccess) return cuda_fail(e, "gated scan kernel launch");
   return MSSM_OK;
 }
@@ -1348,11 +1375,14 @@ mssm_status mssm_gated_scan_bwd(const mssm_tensor* x, const mssm_tensor* r, cons
   a.part = call.Bt > 1 ? static_cast<float*>(workspace->data) : nullptr;
   e = mssm::device_error_word(&a.err);
   if (e != cudaSuccess) return cuda_fail(e, "device error word");
-  int warps = gated_warps(call.Bt * call.D, call.L);
-  if (call.L > (1 << 19)) warps = mssm::kGatedWarps;  // the checkpoints of four rows share 48 KB
-  const int64_t tile = 32 * warps * mssm::kGs;
-  a.ntiles = int((call.L + mssm::kGs + tile - 1) / tile);
-  e = tracked(MSSM_KERNEL_GATED_BWD, s, [&] { return mssm::launch_gated_bwd(a, warps, call.dtype, s); });
+  int dev = -1;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  GatedShape g = gated_shape(call.Bt * call.D, call.L, device_state(dev)->sm_count);
+  if (call.L > (1 << 19) && g.warps < 8) g.warps = 8;  // the checkpoints of a CTA's rows fit 48 KB
+  a.split = g.split;
+  const int64_t tile = int64_t(32) * g.warps * g.split * mssm::kGs;
+  a.ntiles = int((call.L + 8 + tile - 1) / tile);  // rows start at most 8 steps behind a boundary
+  e = tracked(MSSM_KERNEL_GATED_BWD, s, [&] { return mssm::launch_gated_bwd(a, g.warps, call.dtype, s); });
   if (e != cudaSuccess) return cuda_fail(e, "gated backward kernel launch");
   return MSSM_OK;
 }

@@ -13,12 +13,13 @@
 
 #include <cstdint>
 
+#include <cuda_runtime.h>
+
 #include "device_common.cuh"
 
 namespace mssm {
 
 constexpr int kGs = 8;             // steps per thread
-constexpr int kGatedWarps = 4;     // warps per CTA
 constexpr float kResetA = -0.0f;   // the decay of a sequence's first step: composes to "ignore what came before"
 
 struct GatedArgs {
@@ -47,7 +48,8 @@ struct GatedArgs {
   int64_t dh_sb, dh_sd;
   float *dlam, *drb, *dib;         // [D] (biases' may be null)
   float* part;                     // [3, Bt, D] row sums of the three when Bt > 1
-  int ntiles;                      // tiles of a row (backward: checkpoints in shared memory)
+  int ntiles;                      // tiles of a row and CTA (backward: checkpoints in shared memory)
+  int split;                       // CTAs (a cluster) that share a row
 };
 
 struct GatedStepArgs {
@@ -63,18 +65,19 @@ struct GatedStepArgs {
   int Bt, D;
 };
 
-// ---------------------------------------------------------------- scalar pieces
+// ---------------------------------------------------------------- gates and decays
 
-__device__ __forceinline__ float sqrt_approx(float x) {
-  float r;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 __device__ __forceinline__ float rsqrt_approx(float x) {
   float r;
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ f2_t f2s(float v) { return f2(v, v); }
 
 // softplus and the logistic function of a per-channel parameter, once per row: the accurate
 // library functions (the rate's relative error multiplies every decay's logarithm).
@@ -86,132 +89,250 @@ __device__ __forceinline__ float logistic_exact(float v) {
 
 // per-channel constants of a row
 struct GatedRow {
-  float rate;       // c softplus(lam)
-  float rb, ib;
+  float rate;    // c softplus(lam)
+  float cr, ci;  // -log2(e) times the biases
+  bool slow;     // some gate may take rate r past the series of the decay: CARE
 };
+
+constexpr float kSeriesEnd = 0.25f;
+constexpr float kVScale = 1048576.0f;  // 2^20
 
 template <typename Args>
 __device__ __forceinline__ GatedRow gated_row(const Args& p, int d) {
   GatedRow w;
-  const float sp = softplus_exact(p.lam[d * p.lam_s]);
-  w.rate = p.c * sp;
-  w.rb = p.rb ? p.rb[d * p.rb_s] : 0.0f;
-  w.ib = p.ib ? p.ib[d * p.ib_s] : 0.0f;
+  w.rate = p.c * softplus_exact(p.lam[d * p.lam_s]);
+  w.cr = p.rb ? -kLog2e * p.rb[d * p.rb_s] : 0.0f;
+  w.ci = p.ib ? -kLog2e * p.ib[d * p.ib_s] : 0.0f;
+  w.slow = !(w.rate < kSeriesEnd);
   return w;
 }
 
-// The decay a = exp(-y), y = rate r >= 0, and 1 - a^2.  Below y = 1/4, 1 - a is the Taylor series
-// y (1 - y/2 + ... - y^5/720) (first omitted term y^6/5040 < 5e-8 of it), so a is rounded once: a
-// relative error e of a slow decay compounds over its memory to e / y, and the SFU's 2^-22 would be
-// felt.  1 - a^2 = (1 - a)(1 + a) keeps the series' relative accuracy.  Above 1/4, 1 - a >= 0.22
-// and the SFU exponential serves both.
-struct Decay {
-  float a, v;  // v = 1 - a^2
-};
+// Gates of a pair of steps: sigmoid(v) = 1 / (1 + e), e = 2^(-log2(e) v).
+// The usual path (CARE = false) gives the recurrence gate its own reciprocal and lets the input gate and
+// sigmoid(z) share that of their product: 5 SFU results a step instead of 6.  `most` collects what has
+// to stay below 2^125 for it; where it does not, or is a NaN, the window is computed once more with CARE:
+// a reciprocal for each gate, so every gate falls to the smallest normal number before it is zero, and a
+// NaN stays with its own gate.  Rows of fast decays take CARE at once.
+constexpr float kGateMost = 4.2535296e37f;  // 2^125
 
-__device__ __forceinline__ Decay decay(float y) {
-  float q = fmaf(y, -1.0f / 720.0f, 1.0f / 120.0f);
-  q = fmaf(y, q, -1.0f / 24.0f);
-  q = fmaf(y, q, 1.0f / 6.0f);
-  q = fmaf(y, q, -0.5f);
-  q = fmaf(y, q, 1.0f);
-  const float e = ex2f(-kLog2e * y);
-  const bool small = y < 0.25f;
-  const float m = small ? y * q : 1.0f - e;
-  Decay d;
-  d.a = small ? 1.0f - m : e;
-  d.v = fmaf(-m, m, m + m);
-  return d;
+__device__ __forceinline__ f2_t ex2_2(f2_t v) {
+  float a, b;
+  f2split(v, a, b);
+  return f2(ex2f(a), ex2f(b));
+}
+__device__ __forceinline__ f2_t rcp_2(f2_t v) {
+  float a, b;
+  f2split(v, a, b);
+  return f2(rcpf(a), rcpf(b));
+}
+__device__ __forceinline__ void note_most(float& most, f2_t v) {
+  float a, b;
+  f2split(v, a, b);
+  most = max_nan(most, max_nan(a, b));
 }
 
-// The logistic function as e^-|v| / (1 + e^-|v|) or 1 / (1 + e^-|v|): every denominator lies in
-// [1, 2], so several share one reciprocal of their product without overflow.
-struct Gates {
-  float r, i, sz;     // sz: sigmoid(z) with Z
-  float r1, i1, sz1;  // their complements, without the cancellation of 1 - r
-};
-
-template <bool Z, bool COMP = false>
-__device__ __forceinline__ Gates gates(float vr, float vi, float z) {
-  const float er = ex2f(-kLog2e * fabsf(vr)), ei = ex2f(-kLog2e * fabsf(vi));
-  const float nr = vr >= 0.0f ? 1.0f : er, ni = vi >= 0.0f ? 1.0f : ei;
-  const float pr = 1.0f + er, pi = 1.0f + ei;
-  Gates g;
-  if constexpr (Z) {
-    const float ez = ex2f(-kLog2e * fabsf(z));
-    const float nz = z >= 0.0f ? 1.0f : ez, pz = 1.0f + ez;
-    const float ri = pr * pi;
-    const float q = rcpf(ri * pz);
-    const float qz = q * pz;
-    const float fr = pi * qz, fi = pr * qz, fz = ri * q;  // the reciprocals of pr, pi, pz
-    g.r = nr * fr;
-    g.i = ni * fi;
-    g.sz = nz * fz;
-    if (COMP) {
-      g.r1 = (vr >= 0.0f ? er : 1.0f) * fr;
-      g.i1 = (vi >= 0.0f ? ei : 1.0f) * fi;
-      g.sz1 = (z >= 0.0f ? ez : 1.0f) * fz;
-    }
+template <bool Z, bool CARE>
+__device__ __forceinline__ void gate_pair(f2_t rr, f2_t ii, f2_t zz, const GatedRow& w, f2_t& r, f2_t& i, f2_t& sz,
+                                          float& most) {
+  r = rcp_2(add2(ex2_2(fma2(rr, f2s(-kLog2e), f2s(w.cr))), f2s(1.0f)));
+  const f2_t pi = add2(ex2_2(fma2(ii, f2s(-kLog2e), f2s(w.ci))), f2s(1.0f));
+  if constexpr (!Z) {
+    i = rcp_2(pi);
   } else {
-    const float q = rcpf(pr * pi);
-    const float fr = pi * q, fi = pr * q;
-    g.r = nr * fr;
-    g.i = ni * fi;
-    g.sz = 1.0f;
-    if (COMP) {
-      g.r1 = (vr >= 0.0f ? er : 1.0f) * fr;
-      g.i1 = (vi >= 0.0f ? ei : 1.0f) * fi;
-      g.sz1 = 0.0f;
+    const f2_t pz = add2(ex2_2(mul2(zz, f2s(-kLog2e))), f2s(1.0f));
+    if constexpr (CARE) {
+      i = rcp_2(pi);
+      sz = rcp_2(pz);
+    } else {
+      const f2_t both = mul2(pi, pz), q = rcp_2(both);
+      note_most(most, both);
+      i = mul2(q, pz);
+      sz = mul2(q, pi);
     }
   }
-  return g;
+}
+
+// CARE: a sigmoid and its complement, which is 1 long before e / (1 + e) overflows
+__device__ __forceinline__ void sigmoid_both(f2_t v, f2_t& s, f2_t& c) {
+  const f2_t e = ex2_2(v);
+  s = rcp_2(add2(e, f2s(1.0f)));
+  const f2_t q = mul2(e, s);
+  c = f2(f2lo(e) < 1.0e18f ? f2lo(q) : 1.0f, f2hi(e) < 1.0e18f ? f2hi(q) : 1.0f);
+}
+
+// The same with the complements 1 - r, 1 - i, 1 - sigmoid(z) = e / (1 + e), free of the cancellation of
+// 1 - r.
+template <bool Z, bool CARE>
+__device__ __forceinline__ void gate_pair_grad(f2_t rr, f2_t ii, f2_t zz, const GatedRow& w, f2_t& r, f2_t& i, f2_t& sz,
+                                               f2_t& rc, f2_t& ic, f2_t& szc, float& most) {
+  const f2_t ur = fma2(rr, f2s(-kLog2e), f2s(w.cr)), ui = fma2(ii, f2s(-kLog2e), f2s(w.ci));
+  if constexpr (CARE) {
+    sigmoid_both(ur, r, rc);
+    sigmoid_both(ui, i, ic);
+    if constexpr (Z) sigmoid_both(mul2(zz, f2s(-kLog2e)), sz, szc);
+  } else {
+    const f2_t er = ex2_2(ur), ei = ex2_2(ui);
+    const f2_t pr = add2(er, f2s(1.0f)), pi = add2(ei, f2s(1.0f));
+    r = rcp_2(pr);
+    rc = mul2(er, r);
+    note_most(most, pr);
+    if constexpr (Z) {
+      const f2_t ez = ex2_2(mul2(zz, f2s(-kLog2e))), pz = add2(ez, f2s(1.0f));
+      const f2_t both = mul2(pi, pz), q = rcp_2(both);
+      note_most(most, both);
+      i = mul2(q, pz);
+      sz = mul2(q, pi);
+      szc = mul2(ez, sz);
+    } else {
+      note_most(most, pi);
+      i = rcp_2(pi);
+    }
+    ic = mul2(ei, i);
+  }
+}
+
+// The decay a = exp(-y), y = rate r >= 0, and v = 2^20 (1 - a^2).  Below y = 1/4, m = 1 - a is the Taylor series
+// y (1 - y/2 + ... - y^5/720) (first omitted term y^6/5040 < 5e-8 of it), so a is rounded once: a
+// relative error e of a slow decay compounds over its memory to e / y, and the SFU's 2^-22 would be
+// felt.  v = 2^20 m (1 + a) keeps the series' relative accuracy.  Above 1/4, m >= 0.22 and the SFU
+// exponential serves both; only rows whose rate reaches 1/4 (which take CARE) look.
+template <bool CARE>
+__device__ __forceinline__ void decay_pair(f2_t y, f2_t& a, f2_t& v) {
+  f2_t q = fma2(y, f2s(-1.0f / 720.0f), f2s(1.0f / 120.0f));
+  q = fma2(y, q, f2s(-1.0f / 24.0f));
+  q = fma2(y, q, f2s(1.0f / 6.0f));
+  q = fma2(y, q, f2s(-0.5f));
+  q = fma2(y, q, f2s(1.0f));
+  f2_t m = mul2(y, q);
+  a = fma2(m, f2s(-1.0f), f2s(1.0f));
+  if constexpr (CARE) {
+    float y0, y1, m0, m1, a0, a1;
+    f2split(y, y0, y1);
+    f2split(m, m0, m1);
+    f2split(a, a0, a1);
+    const float e0 = ex2f(-kLog2e * y0), e1 = ex2f(-kLog2e * y1);
+    m = f2(y0 < kSeriesEnd ? m0 : 1.0f - e0, y1 < kSeriesEnd ? m1 : 1.0f - e1);
+    a = f2(y0 < kSeriesEnd ? a0 : e0, y1 < kSeriesEnd ? a1 : e1);
+  }
+  v = mul2(m, fma2(a, f2s(kVScale), f2s(kVScale)));
+}
+
+// 2^-20 / sqrt(1 - a^2), so that v times it is sqrt(1 - a^2); finite at v = 0.  The smallest normal number is
+// added to 2^20 v = 2^40 (1 - a^2), where it changes no normal 1 - a^2.
+__device__ __forceinline__ f2_t rsqrt_pair(f2_t v) {
+  float v0, v1;
+  f2split(fma2(v, f2s(kVScale), f2s(1.17549435e-38f)), v0, v1);
+  return f2(rsqrt_approx(v0), rsqrt_approx(v1));
+}
+
+// zeros the steps of a window that `valid` leaves out
+template <int E>
+__device__ __forceinline__ void blank(f2_t (&v)[E / 2], unsigned valid) {
+#pragma unroll
+  for (int k = 0; k < E / 2; ++k)
+    v[k] = f2(valid >> (2 * k) & 1u ? f2lo(v[k]) : 0.0f, valid >> (2 * k + 1) & 1u ? f2hi(v[k]) : 0.0f);
+}
+
+// A window's a, driven terms b = sqrt(1 - a^2) i x and, with Z, silu(z) (in zz).  Returns `most`.
+template <bool Z, bool CARE, int E>
+__device__ __forceinline__ float steps(const f2_t (&x)[E / 2], const f2_t (&rr)[E / 2], const f2_t (&ii)[E / 2],
+                                       f2_t (&zz)[E / 2], const GatedRow& w, float (&av)[E], float (&bv)[E]) {
+  float most = 0.0f;
+#pragma unroll
+  for (int k = 0; k < E / 2; ++k) {
+    f2_t r, i, sz, a, v;
+    gate_pair<Z, CARE>(rr[k], ii[k], zz[k], w, r, i, sz, most);
+    decay_pair<CARE>(mul2(r, f2s(w.rate)), a, v);
+    const f2_t b = mul2(mul2(mul2(v, rsqrt_pair(v)), i), x[k]);
+    f2split(a, av[2 * k], av[2 * k + 1]);
+    f2split(b, bv[2 * k], bv[2 * k + 1]);
+    if (Z) zz[k] = mul2(zz[k], sz);
+  }
+  return most;
+}
+
+// The same for the backward pass.  In: x, r, i, z, dout.  Out: y = rate r (x), 1 - r (r), i x rho (i),
+// dout silu'(z) (z), dout silu(z) (g), sqrt(1 - a^2) i (pv), b (1 - i) (cv), a and b.  `valid`: the steps
+// that count; y is 0 at the others.
+template <bool Z, bool CARE, int E>
+__device__ __forceinline__ float steps_grad(f2_t (&xv)[E / 2], f2_t (&rv)[E / 2], f2_t (&iv)[E / 2], f2_t (&zv)[E / 2],
+                                            f2_t (&gv)[E / 2], const GatedRow& w, bool whole, unsigned valid,
+                                            float (&av)[E], float (&bv)[E], f2_t (&pv)[E / 2], f2_t (&cv)[E / 2]) {
+  float most = 0.0f;
+#pragma unroll
+  for (int k = 0; k < E / 2; ++k) {
+    f2_t rg, ig, sz = 0, rc, ic, szc = 0, a, v;
+    gate_pair_grad<Z, CARE>(rv[k], iv[k], Z ? zv[k] : 0, w, rg, ig, sz, rc, ic, szc, most);
+    f2_t y = mul2(rg, f2s(w.rate));
+    if (!whole) {
+      f2_t one[1] = {y};
+      blank<2>(one, valid >> (2 * k));
+      y = one[0];
+    }
+    decay_pair<CARE>(y, a, v);
+    const f2_t q = rsqrt_pair(v);
+    pv[k] = mul2(mul2(v, q), ig);
+    const f2_t b = mul2(pv[k], xv[k]);
+    iv[k] = mul2(mul2(ig, xv[k]), mul2(a, mul2(mul2(y, f2s(kVScale)), q)));
+    xv[k] = y;
+    rv[k] = rc;
+    cv[k] = mul2(b, ic);
+    if (Z) {
+      const f2_t ds = mul2(gv[k], sz);
+      gv[k] = mul2(ds, zv[k]);
+      zv[k] = mul2(ds, fma2(zv[k], szc, f2s(1.0f)));
+    }
+    f2split(a, av[2 * k], av[2 * k + 1]);
+    f2split(b, bv[2 * k], bv[2 * k + 1]);
+  }
+  return most;
 }
 
 // ---------------------------------------------------------------- a thread's window of a row
 
-// kGs consecutive elements as stored: 16 bytes of bf16 or 32 of fp32
-template <typename T>
+// E consecutive elements as stored
+template <typename T, int E>
 struct Win {
-  static constexpr int kVecs = kGs * int(sizeof(T)) / 16;
+  static constexpr int kVecs = E * int(sizeof(T)) / 16;
   uint4 v[kVecs];
 };
 
-template <typename T>
-__device__ __forceinline__ void win_get(const Win<T>& w, float (&f)[kGs]) {
+// ... and as fp32 pairs
+template <typename T, int E>
+__device__ __forceinline__ void win_get(const Win<T, E>& w, f2_t (&f)[E / 2]) {
   if constexpr (sizeof(T) == 2) {
-    const uint32_t u[4] = {w.v[0].x, w.v[0].y, w.v[0].z, w.v[0].w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      f[2 * k] = bf16lo(u[k]);
-      f[2 * k + 1] = bf16hi(u[k]);
+    for (int k = 0; k < Win<T, E>::kVecs; ++k) {
+      f[4 * k] = f2(bf16lo(w.v[k].x), bf16hi(w.v[k].x));
+      f[4 * k + 1] = f2(bf16lo(w.v[k].y), bf16hi(w.v[k].y));
+      f[4 * k + 2] = f2(bf16lo(w.v[k].z), bf16hi(w.v[k].z));
+      f[4 * k + 3] = f2(bf16lo(w.v[k].w), bf16hi(w.v[k].w));
     }
   } else {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      f[4 * k] = __uint_as_float(w.v[k].x);
-      f[4 * k + 1] = __uint_as_float(w.v[k].y);
-      f[4 * k + 2] = __uint_as_float(w.v[k].z);
-      f[4 * k + 3] = __uint_as_float(w.v[k].w);
+    for (int k = 0; k < Win<T, E>::kVecs; ++k) {
+      f[2 * k] = f2(__uint_as_float(w.v[k].x), __uint_as_float(w.v[k].y));
+      f[2 * k + 1] = f2(__uint_as_float(w.v[k].z), __uint_as_float(w.v[k].w));
     }
   }
 }
 
-// Steps [t0, t0 + kGs) of a row of L steps.  vec: the window's address is 16-byte aligned.  Steps
+// Steps [t0, t0 + E) of a row of L steps.  vec: the window's address is 16-byte aligned.  Steps
 // outside the row are not read and come back as zero.
-template <typename T>
-__device__ __forceinline__ Win<T> win_load(const T* row, int t0, int L, bool vec) {
-  Win<T> w;
-  if (vec && t0 >= 0 && t0 + kGs <= L) {
+template <typename T, int E>
+__device__ __forceinline__ Win<T, E> win_load(const T* row, int t0, int L, bool vec) {
+  Win<T, E> w;
+  if (vec && t0 >= 0 && t0 + E <= L) {
     const uint4* p = reinterpret_cast<const uint4*>(row + t0);
 #pragma unroll
-    for (int k = 0; k < Win<T>::kVecs; ++k) w.v[k] = __ldg(p + k);
+    for (int k = 0; k < Win<T, E>::kVecs; ++k) w.v[k] = __ldg(p + k);
     return w;
   }
-  uint32_t u[4 * Win<T>::kVecs];
+  uint32_t u[4 * Win<T, E>::kVecs];
 #pragma unroll
-  for (int k = 0; k < 4 * Win<T>::kVecs; ++k) u[k] = 0u;
+  for (int k = 0; k < 4 * Win<T, E>::kVecs; ++k) u[k] = 0u;
 #pragma unroll
-  for (int j = 0; j < kGs; ++j) {
+  for (int j = 0; j < E; ++j) {
     const int t = t0 + j;
     if (t < 0 || t >= L) continue;
     if constexpr (sizeof(T) == 2) {
@@ -221,33 +342,36 @@ __device__ __forceinline__ Win<T> win_load(const T* row, int t0, int L, bool vec
     }
   }
 #pragma unroll
-  for (int k = 0; k < Win<T>::kVecs; ++k) w.v[k] = make_uint4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
+  for (int k = 0; k < Win<T, E>::kVecs; ++k) w.v[k] = make_uint4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
   return w;
 }
 
 // Stores the steps of `mask` (bit j: step t0 + j, which lies inside the row).
-template <typename T>
-__device__ __forceinline__ void win_store(T* row, int t0, unsigned mask, bool vec, const float (&f)[kGs]) {
-  if (vec && mask == (1u << kGs) - 1u) {
+template <typename T, int E>
+__device__ __forceinline__ void win_store(T* row, int t0, unsigned mask, bool vec, const f2_t (&f)[E / 2]) {
+  if (vec && mask == (1u << E) - 1u) {
     uint4* p = reinterpret_cast<uint4*>(row + t0);
-    if constexpr (sizeof(T) == 2) {
-      p[0] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                        pack_bf16x2(f[6], f[7]));
-    } else {
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        p[k] = make_uint4(__float_as_uint(f[4 * k]), __float_as_uint(f[4 * k + 1]), __float_as_uint(f[4 * k + 2]),
-                          __float_as_uint(f[4 * k + 3]));
+    for (int k = 0; k < Win<T, E>::kVecs; ++k) {
+      if constexpr (sizeof(T) == 2) {
+        p[k] = make_uint4(pack_bf16x2(f2lo(f[4 * k]), f2hi(f[4 * k])), pack_bf16x2(f2lo(f[4 * k + 1]), f2hi(f[4 * k + 1])),
+                          pack_bf16x2(f2lo(f[4 * k + 2]), f2hi(f[4 * k + 2])),
+                          pack_bf16x2(f2lo(f[4 * k + 3]), f2hi(f[4 * k + 3])));
+      } else {
+        p[k] = make_uint4(__float_as_uint(f2lo(f[2 * k])), __float_as_uint(f2hi(f[2 * k])),
+                          __float_as_uint(f2lo(f[2 * k + 1])), __float_as_uint(f2hi(f[2 * k + 1])));
+      }
     }
     return;
   }
 #pragma unroll
-  for (int j = 0; j < kGs; ++j) {
+  for (int j = 0; j < E; ++j) {
     if (!(mask >> j & 1u)) continue;
+    const float v = j & 1 ? f2hi(f[j / 2]) : f2lo(f[j / 2]);
     if constexpr (sizeof(T) == 2) {
-      row[t0 + j] = f_to_bf16(f[j]);
+      row[t0 + j] = f_to_bf16(v);
     } else {
-      row[t0 + j] = f[j];
+      row[t0 + j] = v;
     }
   }
 }
@@ -262,51 +386,78 @@ __device__ __forceinline__ unsigned misalign(const T* p) {
 // What a window holds of the packed sequences: bit j for step t0 + j.
 struct SeqMask {
   unsigned valid, first, last;  // inside a sequence; its first step; its last step
-  int seq;                      // the sequence of the first valid step (or an index before it)
 };
 
-// The last offset at or before t: the largest j in [lo, S] with cu[j] <= t, lo - 1 if there is none
-// at or after lo.  Whatever the offsets hold, the answer stays in [lo - 1, S].
-__device__ __forceinline__ int seq_find(const int* cu, int S, int t, int lo) {
+// The largest j in [lo, S] with cu[j] <= t, as a sequence: in [0, S) whatever the offsets hold.
+__device__ __forceinline__ int seq_of(const int* cu, int S, int t, int lo) {
   int hi = S + 1;
   while (lo < hi) {
     const int mid = lo + (hi - lo) / 2;
     if (__ldg(cu + mid) <= t) lo = mid + 1;
     else hi = mid;
   }
-  return lo - 1;
-}
-
-__device__ __forceinline__ SeqMask seq_mask(const int* cu, int S, int t0, int L, int& hint) {
-  SeqMask m{0u, 0u, 0u, 0};
-  const int tb = t0 < 0 ? 0 : t0, te = t0 + kGs < L ? t0 + kGs : L;
-  if (tb >= te) return m;
-  int j = seq_find(cu, S, tb, hint);
-  hint = j < 0 ? 0 : j;
-  m.seq = j;
-  int start = j >= 0 ? __ldg(cu + j) : -1;
-  int next = j < S ? __ldg(cu + j + 1) : 0x7fffffff;
-  for (int t = tb; t < te; ++t) {
-    while (next <= t) {  // t enters sequence j (empty ones are passed over)
-      ++j;
-      start = next;
-      next = j < S ? __ldg(cu + j + 1) : 0x7fffffff;
-    }
-    if (j < 0 || j >= S) continue;
-    const unsigned bit = 1u << (t - t0);
-    m.valid |= bit;
-    if (t == start) m.first |= bit;
-    if (t + 1 == next) m.last |= bit;
-  }
-  return m;
-}
-
-// The sequence of step t, searching from the window's index; an index in [0, S) whatever the
-// offsets hold.
-__device__ __forceinline__ int seq_of(const int* cu, int S, int t, int from) {
-  const int j = seq_find(cu, S, t, from < 0 ? 0 : from);
+  const int j = lo - 1;
   return j < 0 ? 0 : j < S ? j : S - 1;
 }
+
+// A warp's walk through the offsets: `before` counts those below the warp's first step, 32 looked at
+// together.  Offsets that are out of order give wrong counts in [0, S + 1] and an end to every loop.
+struct SeqWalk {
+  const int* cu;
+  int S, c0, cS;  // the first and last offset
+  int before;
+
+  __device__ __forceinline__ void start(const int* offsets, int n) {
+    cu = offsets;
+    S = n;
+    c0 = __ldg(cu);
+    cS = __ldg(cu + n);
+    before = 0;
+  }
+  // To the warp's steps [wt, wt + n): counts the offsets below it and says whether it lies inside one
+  // sequence, with no first or last step (up = false: the walk goes back, by bisection).
+  __device__ __forceinline__ bool enter(int wt, int n, int lane, bool up) {
+    if (!up) {
+      int lo = 0;
+      while (lo < before) {
+        const int mid = lo + (before - lo) / 2;
+        if (__ldg(cu + mid) < wt) lo = mid + 1;
+        else before = mid;
+      }
+    }
+    int v;
+    while (true) {
+      v = before + lane <= S ? __ldg(cu + before + lane) : 0x7fffffff;
+      const unsigned below = __ballot_sync(~0u, v < wt);
+      before += __popc(below);
+      if (below != ~0u) break;
+    }
+    return !__any_sync(~0u, v >= wt && v <= wt + n) && before >= 1 && before <= S;
+  }
+  template <int E>
+  __device__ __forceinline__ SeqMask masks(int wt, int t0, int L, int lane) const {
+    SeqMask m{0u, 0u, 0u};
+    constexpr unsigned kAll = (1u << E) - 1u;
+    const int lo = max(max(c0, 0) - t0, 0), hi = min(min(cS, L) - t0, E);
+    if (hi > lo) m.valid = (kAll >> (E - hi)) & ~((1u << lo) - 1u);
+    const int te = wt + 32 * E;
+    for (int at = before;; at += 32) {
+      const int v = at + lane <= S ? __ldg(cu + at + lane) : 0x7fffffff;
+      unsigned in = __ballot_sync(~0u, v >= wt && v <= te);
+      while (in) {
+        const int o = __shfl_sync(~0u, v, __ffs(in) - 1) - t0;
+        in &= in - 1;
+        if (o >= 0 && o < E) m.first |= 1u << o;
+        if (o >= 1 && o <= E) m.last |= 1u << (o - 1);
+      }
+      if (__any_sync(~0u, v > te)) break;
+    }
+    m.first &= m.valid;
+    m.last &= m.valid;
+    return m;
+  }
+  __device__ __forceinline__ int seq(int t) const { return seq_of(cu, S, t, before > 0 ? before - 1 : 0); }
+};
 
 // ---------------------------------------------------------------- composing affine maps
 
@@ -335,34 +486,88 @@ __device__ __forceinline__ void warp_compose(float& a, float& b, int lane) {
   }
 }
 
-// Carries `h` across a tile of W warps: in, the value before the tile; out, after it.  a, b: the
-// thread's map.  Returns the value before the thread's own steps.  buf: 2 * W pairs of shared memory
-// (two sets, used in turn, so one barrier per tile is enough).
-template <bool VL, bool REV, int W>
-__device__ __forceinline__ float tile_carry(float a, float b, float& h, float2* buf, int& flip, int warp, int lane) {
+__device__ __forceinline__ unsigned cluster_rank() {
+  unsigned r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// writes a pair into the same shared-memory place of another CTA of the cluster
+__device__ __forceinline__ void cluster_put(float2* at, unsigned rank, float2 v) {
+  unsigned a = unsigned(__cvta_generic_to_shared(at)), r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(r), "f"(v.x), "f"(v.y) : "memory");
+}
+
+__device__ __forceinline__ void cluster_put1(float* at, unsigned rank, float v) {
+  unsigned a = unsigned(__cvta_generic_to_shared(at)), r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(r), "f"(v) : "memory");
+}
+
+constexpr int kMaxSplit = 8;  // CTAs of a cluster that share a row
+
+// The maps that tiles exchange: two sets, used in turn, so one barrier per exchange is enough.
+template <int W>
+struct CarrySmem {
+  float2 warp[2][W];
+  float2 cta[2][kMaxSplit];
+};
+
+// Carries `h` across a tile of W warps (CL: of a cluster's CTAs): in, the value before the tile; out,
+// after it.  a, b: the thread's map.  Returns the value before the thread's own steps.
+template <bool VL, bool REV, int W, bool CL>
+__device__ __forceinline__ float tile_carry(float a, float b, float& h, CarrySmem<W>& sm, int& flip, int warp, int lane,
+                                            int rank, int split) {
   warp_compose<VL, REV>(a, b, lane);
   float ea = REV ? __shfl_down_sync(~0u, a, 1) : __shfl_up_sync(~0u, a, 1);
   float eb = REV ? __shfl_down_sync(~0u, b, 1) : __shfl_up_sync(~0u, b, 1);
-  if (lane == (REV ? 31 : 0)) ea = 1.0f, eb = 0.0f;
-  const int edge = REV ? 0 : 31;
+  constexpr int edge = REV ? 0 : 31;
+  if (lane == 31 - edge) ea = 1.0f, eb = 0.0f;
   if constexpr (W == 1) {
     const float ta = __shfl_sync(~0u, a, edge), tb = __shfl_sync(~0u, b, edge);
     const float mine = apply<VL>(ea, eb, h);
     h = apply<VL>(ta, tb, h);
     return mine;
   } else {
-    float2* s = buf + flip * W;
-    flip ^= 1;
+    float2* s = sm.warp[flip];
     if (lane == edge) s[warp] = make_float2(a, b);
     __syncthreads();
     float in = h;
+    if constexpr (CL) {
+      // the CTA's map, to every CTA of the cluster
+      if (warp == 0) {
+        float ta = 1.0f, tb = 0.0f;
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+          const float2 m = s[REV ? W - 1 - k : k];
+          float ca = m.x, cb = m.y;
+          compose<VL>(ca, cb, ta, tb);
+          ta = ca;
+          tb = cb;
+        }
+        if (lane < split) cluster_put(&sm.cta[flip][rank], lane, make_float2(ta, tb));
+      }
+      cluster_barrier();
+      for (int k = 0; k < split; ++k) {
+        const int c = REV ? split - 1 - k : k;
+        if (c == rank) in = h;
+        const float2 m = sm.cta[flip][c];
+        h = apply<VL>(m.x, m.y, h);
+      }
+    }
+    float v = in;
 #pragma unroll
     for (int k = 0; k < W; ++k) {
       const int w = REV ? W - 1 - k : k;
-      if (w == warp) in = h;
+      if (w == warp) in = v;
       const float2 m = s[w];
-      h = apply<VL>(m.x, m.y, h);
+      v = apply<VL>(m.x, m.y, v);
     }
+    if constexpr (!CL) h = v;
+    flip ^= 1;
     return apply<VL>(ea, eb, in);
   }
 }
@@ -379,93 +584,142 @@ __device__ __forceinline__ void check_offsets(const int* cu, int S, int L, unsig
   if (bad && err) atomicOr(err, 4u);
 }
 
-template <typename T, bool Z>
+template <typename T, int E, bool Z>
 struct GatedIn {
-  Win<T> x, r, i, z;
+  Win<T, E> x, r, i, z;
 };
 
-// W warps of a CTA share a row; with W == 1 every warp has its own.
-template <typename T, int W, bool Z, bool VL>
-__global__ void __launch_bounds__(32 * kGatedWarps) gated_scan_kernel(const GatedArgs p) {
-  constexpr int kRows = kGatedWarps / W;
-  __shared__ float2 s_buf[2 * kGatedWarps];
+constexpr int gated_threads(int W) { return W == 1 ? 128 : 32 * W; }
+
+// the steps of a plain row's window that lie inside the row
+template <int E>
+__device__ __forceinline__ unsigned row_mask(int t0, int L) {
+  const int lo = max(-t0, 0), hi = min(L - t0, E);
+  return hi > lo ? ((1u << E) - 1u) >> (E - hi) & ~((1u << lo) - 1u) : 0u;
+}
+
+// W warps of a CTA share a row, with CL the CTAs of a cluster do; with W == 1 every warp has its own.
+template <typename T, int E, int W, bool Z, bool VL, bool CL>
+__global__ void __launch_bounds__(gated_threads(W)) gated_scan_kernel(const GatedArgs p) {
+  constexpr int kRows = W == 1 ? 4 : 1;
+  __shared__ CarrySmem<W> sm;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (VL && blockIdx.x == 0) check_offsets(p.cu, p.S, p.L, p.err);
-  const int64_t row = int64_t(blockIdx.x) * kRows + (W == 1 ? warp : 0);
+  const int split = CL ? p.split : 1, rank = CL ? int(cluster_rank()) : 0;
+  const int64_t row = CL ? blockIdx.x / split : int64_t(blockIdx.x) * kRows + (W == 1 ? warp : 0);
   if (row >= int64_t(p.Bt) * p.D) return;
   const int bt = int(row / p.D), d = int(row % p.D);
-  const int wr = W == 1 ? 0 : warp;
+  const int wr = (W == 1 ? 0 : warp) + rank * W;  // the warp's place among those of the row
   const T* x = static_cast<const T*>(p.x) + bt * p.x_sb + d * p.x_sd;
   const T* r = static_cast<const T*>(p.r) + bt * p.r_sb + d * p.r_sd;
   const T* i = static_cast<const T*>(p.i) + bt * p.i_sb + d * p.i_sd;
   const T* z = Z ? static_cast<const T*>(p.z) + bt * p.z_sb + d * p.z_sd : nullptr;
   T* out = static_cast<T*>(p.out) + bt * p.o_sb + d * p.o_sd;
   const GatedRow w = gated_row(p, d);
+  if (CL) cluster_barrier();  // every CTA's shared memory is there
   // windows start on 16-byte boundaries when every tensor's row is equally far from one
   const unsigned mis = misalign(x);
   const bool vec = misalign(r) == mis && misalign(i) == mis && misalign(out) == mis && (!Z || misalign(z) == mis);
   const int off = vec ? int(mis / sizeof(T)) : 0;
   float h = 0.0f;
   if (!VL && p.h0) h = p.h0[bt * p.h0_sb + d * p.h0_sd];
-  if (VL && p.last) {
-    for (int j = wr * 32 + lane; j < p.S; j += 32 * W)
-      if (p.cu[j] >= p.cu[j + 1])
-        p.last[j * p.ls_sb + d * p.ls_sd] = p.h0 ? p.h0[j * p.h0_sb + d * p.h0_sd] : 0.0f;
+  SeqWalk walk;
+  if (VL) {
+    walk.start(p.cu, p.S);
+    if (p.last)
+      for (int j = wr * 32 + lane; j < p.S; j += 32 * W * split)
+        if (p.cu[j] >= p.cu[j + 1])
+          p.last[j * p.ls_sb + d * p.ls_sd] = p.h0 ? p.h0[j * p.h0_sb + d * p.h0_sd] : 0.0f;
   }
-  int flip = 0, hint = 0;
-  const int tile = 32 * W * kGs;
-  int t0 = (wr * 32 + lane) * kGs - off;
-  GatedIn<T, Z> nx;
+  int flip = 0;
+  const int tile = 32 * W * E * split;
+  int wt = wr * 32 * E - off;
+  GatedIn<T, E, Z> nx;
   auto fetch = [&](int t) {
-    nx.x = win_load(x, t, p.L, vec);
-    nx.r = win_load(r, t, p.L, vec);
-    nx.i = win_load(i, t, p.L, vec);
-    if (Z) nx.z = win_load(z, t, p.L, vec);
+    nx.x = win_load<T, E>(x, t, p.L, vec);
+    nx.r = win_load<T, E>(r, t, p.L, vec);
+    nx.i = win_load<T, E>(i, t, p.L, vec);
+    if (Z) nx.z = win_load<T, E>(z, t, p.L, vec);
   };
-  fetch(t0);
-  for (int base = -off; base < p.L; base += tile, t0 += tile) {
-    float xv[kGs], rv[kGs], iv[kGs], zv[kGs], av[kGs], bv[kGs];
-    win_get(nx.x, xv);
-    win_get(nx.r, rv);
-    win_get(nx.i, iv);
-    if (Z) win_get(nx.z, zv);
-    if (base + tile < p.L) fetch(t0 + tile);
-    SeqMask m;
-    if (VL) {
-      m = seq_mask(p.cu, p.S, t0, p.L, hint);
-    } else {
-      const int lo = t0 < 0 ? -t0 : 0, n = p.L - t0 < kGs ? p.L - t0 : kGs;  // steps [lo, n) of the window
-      m.valid = n > lo ? ((1u << n) - 1u) & ~((1u << lo) - 1u) : 0u;
+  fetch(wt + lane * E);
+  for (int base = -off; base < p.L; base += tile, wt += tile) {
+    const int t0 = wt + lane * E;
+    f2_t xv[E / 2], rv[E / 2], iv[E / 2], zv[E / 2];
+    SeqMask m{(1u << E) - 1u, 0u, 0u};
+    bool whole = wt >= 0 && wt + 32 * E <= p.L;
+    if (VL) whole = walk.enter(wt, 32 * E, lane, true) && whole;
+    if (!whole) {
+      if (VL) m = walk.template masks<E>(wt, t0, p.L, lane);
+      else m.valid = row_mask<E>(t0, p.L);
     }
-    float A = 1.0f, B = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kGs; ++k) {
-      const Gates g = gates<Z>(rv[k] + w.rb, iv[k] + w.ib, Z ? zv[k] : 0.0f);
-      const Decay dc = decay(w.rate * g.r);
-      const float a = dc.a, beta = sqrt_approx(dc.v);
-      if (Z) zv[k] *= g.sz;
-      const bool ok = m.valid >> k & 1u;
-      av[k] = ok ? a : 1.0f;
-      bv[k] = ok ? beta * (g.i * xv[k]) : 0.0f;
-      if (VL && (m.first >> k & 1u)) {
-        if (p.h0) bv[k] = fmaf(a, p.h0[int64_t(seq_of(p.cu, p.S, t0 + k, m.seq)) * p.h0_sb + d * p.h0_sd], bv[k]);
-        av[k] = kResetA;
+    auto unpack = [&] {
+      win_get(nx.x, xv);
+      win_get(nx.r, rv);
+      win_get(nx.i, iv);
+      if (Z) win_get(nx.z, zv);
+      if (!whole) {  // steps outside count as zeros, whatever the tensors hold there
+        blank<E>(xv, m.valid);
+        blank<E>(rv, m.valid);
+        blank<E>(iv, m.valid);
+        if (Z) blank<E>(zv, m.valid);
       }
-      float ca = av[k], cb = bv[k];
-      compose<VL>(ca, cb, A, B);
-      A = ca;
-      B = cb;
+    };
+    unpack();
+    if (base + tile < p.L) fetch(t0 + tile);
+    float av[E], bv[E];
+    float A = 1.0f, B = 0.0f;
+    if (w.slow) {
+      steps<Z, true, E>(xv, rv, iv, zv, w, av, bv);
+    } else if (!(steps<Z, false, E>(xv, rv, iv, zv, w, av, bv) < kGateMost)) {
+      fetch(t0);
+      unpack();
+      if (base + tile < p.L) fetch(t0 + tile);
+      steps<Z, true, E>(xv, rv, iv, zv, w, av, bv);
     }
-    float hk = tile_carry<VL, false, W>(A, B, h, s_buf, flip, wr, lane);
-    float ov[kGs];
+    if (whole) {
 #pragma unroll
-    for (int k = 0; k < kGs; ++k) {
-      hk = apply<VL>(av[k], bv[k], hk);
-      if (VL && (m.last >> k & 1u) && p.last)
-        p.last[int64_t(seq_of(p.cu, p.S, t0 + k, m.seq)) * p.ls_sb + d * p.ls_sd] = hk;
-      ov[k] = Z ? hk * zv[k] : hk;
+      for (int k = 0; k < E; ++k) {
+        B = fmaf(av[k], B, bv[k]);
+        A *= av[k];
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < E; ++k) {
+        if (!(m.valid >> k & 1u)) av[k] = 1.0f, bv[k] = 0.0f;
+        if (VL && (m.first >> k & 1u)) {
+          if (p.h0) bv[k] = fmaf(av[k], p.h0[int64_t(walk.seq(t0 + k)) * p.h0_sb + d * p.h0_sd], bv[k]);
+          av[k] = kResetA;
+        }
+        float ca = av[k], cb = bv[k];
+        compose<VL>(ca, cb, A, B);
+        A = ca;
+        B = cb;
+      }
     }
-    win_store(out, t0, m.valid, vec, ov);
+    float hk = tile_carry<VL, false, W, CL>(A, B, h, sm, flip, W == 1 ? 0 : warp, lane, rank, split);
+    f2_t ov[E / 2];
+    if (!VL || whole) {
+#pragma unroll
+      for (int k = 0; k < E / 2; ++k) {
+        const float h0 = fmaf(av[2 * k], hk, bv[2 * k]);
+        hk = fmaf(av[2 * k + 1], h0, bv[2 * k + 1]);
+        ov[k] = Z ? mul2(f2(h0, hk), zv[k]) : f2(h0, hk);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < E / 2; ++k) {
+        float o[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int e = 2 * k + q;
+          hk = apply<VL>(av[e], bv[e], hk);
+          if ((m.last >> e & 1u) && p.last) p.last[int64_t(walk.seq(t0 + e)) * p.ls_sb + d * p.ls_sd] = hk;
+          o[q] = hk;
+        }
+        ov[k] = Z ? mul2(f2(o[0], o[1]), zv[k]) : f2(o[0], o[1]);
+      }
+    }
+    win_store<T, E>(out, t0, m.valid, vec, ov);
   }
   if (!VL && p.last && lane == 0 && wr == 0) p.last[bt * p.ls_sb + d * p.ls_sd] = h;
 }
@@ -474,25 +728,28 @@ __global__ void __launch_bounds__(32 * kGatedWarps) gated_scan_kernel(const Gate
 
 // dout -> gradients.  With q_t = dout_t silu(z_t), s_t = dLoss/dh_t obeys
 //   s_t = q_t + c_(t+1),  c_t = a_t s_t                  (c: what flows into h_(t-1))
-// and, with la = log a = -rate r, rho = -la / beta (0 where la = 0):
-//   w_t = s_t (la a h_(t-1) + a^2 i x rho)               dLoss/d log(rate) of the step
+// and, with y = rate r = -log a, rho = a y / beta (0 where y = 0):
+//   w_t = s_t a (i x rho - y h_(t-1))                    dLoss/d log(rate) of the step
 //   dr_raw = (1 - r) w, dlam = sigmoid(lam) / softplus(lam) * sum_t w_t
 //   di_raw = s beta x i (1 - i), dx = s beta i, dz = dout h silu'(z)
-// (d beta / d la = -a^2 / beta; written with la inside, nothing is singular at la = 0).
+// (d beta / d y = a^2 / beta; written with y inside, nothing is singular at y = 0).
 // The row is swept forward once, keeping the state before every tile, then backwards tile by tile,
-// recomputing the states inside the tile: the second read finds the row in L2.
-template <typename T, int W, bool Z, bool VL>
-__global__ void __launch_bounds__(32 * kGatedWarps) gated_bwd_kernel(const GatedArgs p) {
-  constexpr int kRows = kGatedWarps / W;
-  __shared__ float2 s_buf[2 * kGatedWarps];
-  __shared__ float s_red[3 * kGatedWarps];
+// recomputing the states inside the tile: the second read finds the row in L2.  A row of one tile is
+// read once.
+template <typename T, int E, int W, bool Z, bool VL, bool CL>
+__global__ void __launch_bounds__(gated_threads(W)) gated_bwd_kernel(const GatedArgs p) {
+  constexpr int kRows = W == 1 ? 4 : 1;
+  __shared__ CarrySmem<W> sm;
+  __shared__ float s_red[3][W];
+  __shared__ float s_sum[3][kMaxSplit];
   extern __shared__ float s_ckpt[];  // [kRows][ntiles]
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (VL && blockIdx.x == 0) check_offsets(p.cu, p.S, p.L, p.err);
-  const int64_t row = int64_t(blockIdx.x) * kRows + (W == 1 ? warp : 0);
+  const int split = CL ? p.split : 1, rank = CL ? int(cluster_rank()) : 0;
+  const int64_t row = CL ? blockIdx.x / split : int64_t(blockIdx.x) * kRows + (W == 1 ? warp : 0);
   if (row >= int64_t(p.Bt) * p.D) return;
   const int bt = int(row / p.D), d = int(row % p.D);
-  const int wr = W == 1 ? 0 : warp;
+  const int wc = W == 1 ? 0 : warp, wr = wc + rank * W;
   float* ckpt = s_ckpt + (W == 1 ? warp * p.ntiles : 0);
   const T* x = static_cast<const T*>(p.x) + bt * p.x_sb + d * p.x_sd;
   const T* r = static_cast<const T*>(p.r) + bt * p.r_sb + d * p.r_sd;
@@ -504,169 +761,235 @@ __global__ void __launch_bounds__(32 * kGatedWarps) gated_bwd_kernel(const Gated
   T* di = static_cast<T*>(p.di) + bt * p.di_sb + d * p.di_sd;
   T* dz = Z ? static_cast<T*>(p.dz) + bt * p.dz_sb + d * p.dz_sd : nullptr;
   const GatedRow w = gated_row(p, d);
+  if (CL) cluster_barrier();
   const unsigned mis = misalign(x);
   const bool vec = misalign(r) == mis && misalign(i) == mis && misalign(gy) == mis && misalign(dx) == mis &&
                    misalign(dr) == mis && misalign(di) == mis && (!Z || (misalign(z) == mis && misalign(dz) == mis));
   const int off = vec ? int(mis / sizeof(T)) : 0;
-  if (VL && p.dh0) {
-    for (int j = wr * 32 + lane; j < p.S; j += 32 * W)
-      if (p.cu[j] >= p.cu[j + 1])
-        p.dh0[j * p.dh_sb + d * p.dh_sd] = p.dlast ? p.dlast[j * p.dl_sb + d * p.dl_sd] : 0.0f;
+  SeqWalk walk;
+  if (VL) {
+    walk.start(p.cu, p.S);
+    if (p.dh0)
+      for (int j = wr * 32 + lane; j < p.S; j += 32 * W * split)
+        if (p.cu[j] >= p.cu[j + 1])
+          p.dh0[j * p.dh_sb + d * p.dh_sd] = p.dlast ? p.dlast[j * p.dl_sb + d * p.dl_sd] : 0.0f;
   }
-  const int tile = 32 * W * kGs;
+  const int tile = 32 * W * E * split;
   const int ntiles = (p.L + off + tile - 1) / tile;
+  const int lane0 = wr * 32 * E - off;  // the warp's first step in the first tile
   int flip = 0;
-  float av[kGs], bv[kGs], hp[kGs];
-
-  // a, the driven term and the masks of the window at t0
-  auto masks = [&](int t0, int& hint) {
-    SeqMask m{0u, 0u, 0u, 0};
-    if (VL) {
-      m = seq_mask(p.cu, p.S, t0, p.L, hint);
-    } else {
-      const int lo = t0 < 0 ? -t0 : 0, n = p.L - t0 < kGs ? p.L - t0 : kGs;
-      m.valid = n > lo ? ((1u << n) - 1u) & ~((1u << lo) - 1u) : 0u;
-      if (p.L - 1 >= t0 && p.L - 1 < t0 + kGs) m.last = 1u << (p.L - 1 - t0);
-    }
-    return m;
-  };
 
   // forward sweep: the state before every tile
+  float h = !VL && p.h0 ? p.h0[bt * p.h0_sb + d * p.h0_sd] : 0.0f;
   {
-    float h = !VL && p.h0 ? p.h0[bt * p.h0_sb + d * p.h0_sd] : 0.0f;
-    int hint = 0;
-    for (int tl = 0; tl < ntiles; ++tl) {
-      if (lane == 0 && wr == 0) ckpt[tl] = h;
-      if (tl + 1 == ntiles) break;
-      const int t0 = tl * tile + (wr * 32 + lane) * kGs - off;
-      float xv[kGs], rv[kGs], iv[kGs];
-      win_get(win_load(x, t0, p.L, vec), xv);
-      win_get(win_load(r, t0, p.L, vec), rv);
-      win_get(win_load(i, t0, p.L, vec), iv);
-      const SeqMask m = masks(t0, hint);
+    GatedIn<T, E, false> nx;
+    auto fetch = [&](int t) {
+      nx.x = win_load<T, E>(x, t, p.L, vec);
+      nx.r = win_load<T, E>(r, t, p.L, vec);
+      nx.i = win_load<T, E>(i, t, p.L, vec);
+    };
+    if (ntiles > 1) fetch(lane0 + lane * E);
+    for (int tl = 0; tl + 1 < ntiles; ++tl) {
+      if (lane == 0 && wc == 0) ckpt[tl] = h;
+      const int wt = lane0 + tl * tile, t0 = wt + lane * E;
+      f2_t xv[E / 2], rv[E / 2], iv[E / 2];
+      win_get(nx.x, xv);
+      win_get(nx.r, rv);
+      win_get(nx.i, iv);
+      if (tl + 2 < ntiles) fetch(t0 + tile);
+      float av[E], bv[E];
       float A = 1.0f, B = 0.0f;
+      bool whole = wt >= 0;  // only the last tile reaches the row's end
+      if (VL) whole = walk.enter(wt, 32 * E, lane, true) && whole;
+      f2_t none[E / 2];
+      if (w.slow) steps<false, true, E>(xv, rv, iv, none, w, av, bv);
+      else steps<false, false, E>(xv, rv, iv, none, w, av, bv);
+      if (whole) {
 #pragma unroll
-      for (int k = 0; k < kGs; ++k) {
-        const Gates g = gates<false>(rv[k] + w.rb, iv[k] + w.ib, 0.0f);
-        const Decay dc = decay(w.rate * g.r);
-        const float a = dc.a, beta = sqrt_approx(dc.v);
-        const bool ok = m.valid >> k & 1u;
-        float ca = ok ? a : 1.0f, cb = ok ? beta * (g.i * xv[k]) : 0.0f;
-        if (VL && (m.first >> k & 1u)) {
-          if (p.h0) cb = fmaf(a, p.h0[int64_t(seq_of(p.cu, p.S, t0 + k, m.seq)) * p.h0_sb + d * p.h0_sd], cb);
-          ca = kResetA;
+        for (int k = 0; k < E; ++k) {
+          B = fmaf(av[k], B, bv[k]);
+          A *= av[k];
         }
-        compose<VL>(ca, cb, A, B);
-        A = ca;
-        B = cb;
+      } else {
+        SeqMask m{0u, 0u, 0u};
+        if (VL) m = walk.template masks<E>(wt, t0, p.L, lane);
+        else m.valid = row_mask<E>(t0, p.L);
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+          if (!(m.valid >> k & 1u)) av[k] = 1.0f, bv[k] = 0.0f;
+          if (VL && (m.first >> k & 1u)) {
+            if (p.h0) bv[k] = fmaf(av[k], p.h0[int64_t(walk.seq(t0 + k)) * p.h0_sb + d * p.h0_sd], bv[k]);
+            av[k] = kResetA;
+          }
+          float ca = av[k], cb = bv[k];
+          compose<VL>(ca, cb, A, B);
+          A = ca;
+          B = cb;
+        }
       }
-      tile_carry<VL, false, W>(A, B, h, s_buf, flip, wr, lane);
+      tile_carry<VL, false, W, CL>(A, B, h, sm, flip, wc, lane, rank, split);
     }
+    if (lane == 0 && wc == 0 && ntiles > 0) ckpt[ntiles - 1] = h;
   }
   if (W == 1) __syncwarp();
   else __syncthreads();
 
   // backward sweep
   float sum_w = 0.0f, sum_r = 0.0f, sum_i = 0.0f;
-  float c = 0.0f;
+  float c = !VL && p.dlast ? p.dlast[bt * p.dl_sb + d * p.dl_sd] : 0.0f;
+  GatedIn<T, E, Z> nx;
+  Win<T, E> ng;
+  auto fetch = [&](int t) {
+    nx.x = win_load<T, E>(x, t, p.L, vec);
+    nx.r = win_load<T, E>(r, t, p.L, vec);
+    nx.i = win_load<T, E>(i, t, p.L, vec);
+    ng = win_load<T, E>(gy, t, p.L, vec);
+    if (Z) nx.z = win_load<T, E>(z, t, p.L, vec);
+  };
+  if (ntiles > 0) fetch(lane0 + (ntiles - 1) * tile + lane * E);
   for (int tl = ntiles - 1; tl >= 0; --tl) {
-    const int t0 = tl * tile + (wr * 32 + lane) * kGs - off;
-    float xv[kGs], rv[kGs], iv[kGs], zv[kGs], gv[kGs], bet[kGs], rho[kGs], yv[kGs], i1[kGs];
-    win_get(win_load(x, t0, p.L, vec), xv);
-    win_get(win_load(r, t0, p.L, vec), rv);
-    win_get(win_load(i, t0, p.L, vec), iv);
-    win_get(win_load(gy, t0, p.L, vec), gv);
-    if (Z) win_get(win_load(z, t0, p.L, vec), zv);
-    int hint = 0;
-    const SeqMask m = masks(t0, hint);
+    const int wt = lane0 + tl * tile, t0 = wt + lane * E;
+    f2_t xv[E / 2], rv[E / 2], iv[E / 2], zv[E / 2], gv[E / 2];
+    SeqMask m{(1u << E) - 1u, 0u, 0u};
+    bool whole = wt >= 0 && wt + 32 * E <= p.L;
+    if (VL) whole = walk.enter(wt, 32 * E, lane, false) && whole;
+    if (!whole) {
+      if (VL) m = walk.template masks<E>(wt, t0, p.L, lane);
+      else m.valid = row_mask<E>(t0, p.L);
+    }
+    auto unpack = [&] {
+      win_get(nx.x, xv);
+      win_get(nx.r, rv);
+      win_get(nx.i, iv);
+      win_get(ng, gv);
+      if (Z) win_get(nx.z, zv);
+      if (!whole) {  // steps outside count as zeros, whatever the tensors hold there
+        blank<E>(xv, m.valid);
+        blank<E>(rv, m.valid);
+        blank<E>(iv, m.valid);
+        blank<E>(gv, m.valid);
+        if (Z) blank<E>(zv, m.valid);
+      }
+    };
+    unpack();
+    if (tl > 0) fetch(t0 - tile);
+    float av[E], bv[E];
+    f2_t pv[E / 2], cv[E / 2];
     float A = 1.0f, B = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kGs; ++k) {
-      const Gates g = gates<Z, true>(rv[k] + w.rb, iv[k] + w.ib, Z ? zv[k] : 0.0f);
-      const float y = w.rate * g.r;
-      const Decay dc = decay(y);
-      const float a = dc.a;
-      const float q = dc.v > 0.0f ? rsqrt_approx(dc.v) : 0.0f;
-      bet[k] = dc.v * q;
-      rho[k] = a * y * q;  // a rho
-      yv[k] = y;
-      rv[k] = g.r1;
-      iv[k] = g.i;
-      i1[k] = g.i1;
-      if (Z) {
-        // zv: dout silu'(z) (then times h); gv: dout silu(z)
-        const float dy = gv[k];
-        gv[k] = dy * zv[k] * g.sz;
-        zv[k] = dy * g.sz * fmaf(zv[k], g.sz1, 1.0f);
-      }
-      const bool ok = m.valid >> k & 1u;
-      av[k] = ok ? a : 1.0f;
-      bv[k] = ok ? bet[k] * (g.i * xv[k]) : 0.0f;
-      hp[k] = 0.0f;
-      if (VL && (m.first >> k & 1u) && p.h0)
-        hp[k] = p.h0[int64_t(seq_of(p.cu, p.S, t0 + k, m.seq)) * p.h0_sb + d * p.h0_sd];
-      float ca = av[k], cb = bv[k];
-      if (VL && (m.first >> k & 1u)) {
-        cb = fmaf(a, hp[k], cb);
-        ca = kResetA;
-      }
-      compose<VL>(ca, cb, A, B);
-      A = ca;
-      B = cb;
+    if (w.slow) {
+      steps_grad<Z, true, E>(xv, rv, iv, zv, gv, w, whole, m.valid, av, bv, pv, cv);
+    } else if (!(steps_grad<Z, false, E>(xv, rv, iv, zv, gv, w, whole, m.valid, av, bv, pv, cv) < kGateMost)) {
+      fetch(t0);
+      unpack();
+      if (tl > 0) fetch(t0 - tile);
+        steps_grad<Z, true, E>(xv, rv, iv, zv, gv, w, whole, m.valid, av, bv, pv, cv);
     }
-    float hin = ckpt[tl];
-    float hk = tile_carry<VL, false, W>(A, B, hin, s_buf, flip, wr, lane);
-    // states before every step, and the adjoint's map of the window
+    float hk;
+    if (!VL || whole) {
 #pragma unroll
-    for (int k = 0; k < kGs; ++k) {
-      if (!(VL && (m.first >> k & 1u))) hp[k] = hk;
-      hk = fmaf(av[k], hp[k], bv[k]);
-      if (Z) zv[k] *= hk;
-    }
-    A = 1.0f;
-    B = 0.0f;
-#pragma unroll
-    for (int k = kGs - 1; k >= 0; --k) {
-      if (!(m.valid >> k & 1u)) gv[k] = 0.0f;
-      if ((m.last >> k & 1u) && p.dlast) {
-        const int64_t sq = VL ? seq_of(p.cu, p.S, t0 + k, m.seq) : bt;
-        gv[k] += p.dlast[sq * p.dl_sb + d * p.dl_sd];
+      for (int k = 0; k < E; ++k) {
+        B = fmaf(av[k], B, bv[k]);
+        A *= av[k];
       }
-      float ca = av[k], cb = av[k] * gv[k];
-      if (VL && (m.last >> k & 1u)) ca = kResetA;
-      compose<VL>(ca, cb, A, B);
-      A = ca;
-      B = cb;
-    }
-    float ck = tile_carry<VL, true, W>(A, B, c, s_buf, flip, wr, lane);
+      float hin = ckpt[tl];
+      hk = tile_carry<VL, false, W, CL>(A, B, hin, sm, flip, wc, lane, rank, split);
+      // w / s = a (i x rho - y h_before), the outputs' gradients, and the adjoint's map of the window
 #pragma unroll
-    for (int k = kGs - 1; k >= 0; --k) {
-      const float s = (VL && (m.last >> k & 1u)) ? gv[k] : gv[k] + ck;
-      const float a = av[k];
-      ck = a * s;
+      for (int k = 0; k < E / 2; ++k) {
+        const float h0 = fmaf(av[2 * k], hk, bv[2 * k]), h1 = fmaf(av[2 * k + 1], h0, bv[2 * k + 1]);
+        const f2_t y = xv[k];
+        xv[k] = mul2(f2(av[2 * k], av[2 * k + 1]), fma2(mul2(y, f2s(-1.0f)), f2(hk, h0), iv[k]));
+        if (Z) zv[k] = mul2(zv[k], f2(h0, h1));
+        hk = h1;
+      }
+      A = 1.0f;
+      B = 0.0f;
+#pragma unroll
+      for (int k = E - 1; k >= 0; --k) {
+        const float g = k & 1 ? f2hi(gv[k / 2]) : f2lo(gv[k / 2]);
+        B = av[k] * (g + B);
+        A *= av[k];
+      }
+    } else {
+      float hb[E];
+#pragma unroll
+      for (int k = 0; k < E; ++k) {
+        hb[k] = 0.0f;
+        float ca = av[k], cb = bv[k];
+        if (m.first >> k & 1u) {
+          if (p.h0) hb[k] = p.h0[int64_t(walk.seq(t0 + k)) * p.h0_sb + d * p.h0_sd];
+          cb = fmaf(ca, hb[k], cb);
+          ca = kResetA;
+        }
+        compose<VL>(ca, cb, A, B);
+        A = ca;
+        B = cb;
+      }
+      float hin = ckpt[tl];
+      hk = tile_carry<VL, false, W, CL>(A, B, hin, sm, flip, wc, lane, rank, split);
+#pragma unroll
+      for (int k = 0; k < E; ++k) {
+        if (!(m.first >> k & 1u)) hb[k] = hk;
+        hk = fmaf(av[k], hb[k], bv[k]);
+        if (!(m.valid >> k & 1u)) hk = hb[k] = 0.0f;  // outside every sequence
+        bv[k] = hk;
+      }
+#pragma unroll
+      for (int k = 0; k < E / 2; ++k) {
+        xv[k] = mul2(f2(av[2 * k], av[2 * k + 1]), fma2(mul2(xv[k], f2s(-1.0f)), f2(hb[2 * k], hb[2 * k + 1]), iv[k]));
+        if (Z) zv[k] = mul2(zv[k], f2(bv[2 * k], bv[2 * k + 1]));
+      }
+      A = 1.0f;
+      B = 0.0f;
+#pragma unroll
+      for (int k = E - 1; k >= 0; --k) {
+        float g = k & 1 ? f2hi(gv[k / 2]) : f2lo(gv[k / 2]);
+        const bool end = m.last >> k & 1u;
+        if (end && p.dlast) {
+          g += p.dlast[int64_t(walk.seq(t0 + k)) * p.dl_sb + d * p.dl_sd];
+          gv[k / 2] = k & 1 ? f2(f2lo(gv[k / 2]), g) : f2(g, f2hi(gv[k / 2]));
+        }
+        float ca = end ? kResetA : av[k], cb = av[k] * g;
+        compose<VL>(ca, cb, A, B);
+        A = ca;
+        B = cb;
+      }
+    }
+    float ck = tile_carry<VL, true, W, CL>(A, B, c, sm, flip, wc, lane, rank, split);
+    float sv[E];
+#pragma unroll
+    for (int k = E - 1; k >= 0; --k) {
+      const float g = k & 1 ? f2hi(gv[k / 2]) : f2lo(gv[k / 2]);
+      sv[k] = VL && (m.last >> k & 1u) ? g : g + ck;
+      ck = av[k] * sv[k];
       if (VL && (m.first >> k & 1u) && p.dh0)
-        p.dh0[int64_t(seq_of(p.cu, p.S, t0 + k, m.seq)) * p.dh_sb + d * p.dh_sd] = ck;
-      const float ix = iv[k] * xv[k];
-      const float ww = s * a * fmaf(ix, rho[k], -yv[k] * hp[k]);
-      const float sb = s * bet[k];
-      const float gr = rv[k] * ww;
-      const float gi = sb * ix * i1[k];
-      if (m.valid >> k & 1u) {
-        sum_w += ww;
-        sum_r += gr;
-        sum_i += gi;
-      }
-      xv[k] = sb * iv[k];
-      rv[k] = gr;
-      iv[k] = gi;
+        p.dh0[int64_t(walk.seq(t0 + k)) * p.dh_sb + d * p.dh_sd] = ck;
+      if (VL && !whole && !(m.valid >> k & 1u)) sv[k] = 0.0f;  // what flows past the steps outside stays out of the sums
     }
-    win_store(dx, t0, m.valid, vec, xv);
-    win_store(dr, t0, m.valid, vec, rv);
-    win_store(di, t0, m.valid, vec, iv);
-    if (Z) win_store(dz, t0, m.valid, vec, zv);
+    f2_t acc_w = 0, acc_r = 0, acc_i = 0;
+#pragma unroll
+    for (int k = 0; k < E / 2; ++k) {
+      const f2_t s = f2(sv[2 * k], sv[2 * k + 1]);
+      const f2_t ww = mul2(s, xv[k]);
+      const f2_t gr = mul2(rv[k], ww);
+      const f2_t gx = mul2(s, pv[k]);
+      const f2_t gi = mul2(s, cv[k]);
+      acc_w = add2(acc_w, ww);
+      acc_r = add2(acc_r, gr);
+      acc_i = add2(acc_i, gi);
+      rv[k] = gr;
+      xv[k] = gx;
+      cv[k] = gi;
+    }
+    win_store<T, E>(dx, t0, m.valid, vec, xv);
+    win_store<T, E>(dr, t0, m.valid, vec, rv);
+    if (Z) win_store<T, E>(dz, t0, m.valid, vec, zv);
+    win_store<T, E>(di, t0, m.valid, vec, cv);
+    sum_w += f2lo(acc_w) + f2hi(acc_w);
+    sum_r += f2lo(acc_r) + f2hi(acc_r);
+    sum_i += f2lo(acc_i) + f2hi(acc_i);
   }
-  if (!VL && p.dh0 && lane == 0 && wr == 0)
-    p.dh0[bt * p.dh_sb + d * p.dh_sd] = ntiles ? c : (p.dlast ? p.dlast[bt * p.dl_sb + d * p.dl_sd] : 0.0f);
+  if (!VL && p.dh0 && lane == 0 && wr == 0) p.dh0[bt * p.dh_sb + d * p.dh_sd] = c;
 
   // the row's sums, in a fixed order
 #pragma unroll
@@ -677,17 +1000,34 @@ __global__ void __launch_bounds__(32 * kGatedWarps) gated_bwd_kernel(const Gated
   }
   if constexpr (W > 1) {
     if (lane == 0) {
-      s_red[warp] = sum_w;
-      s_red[W + warp] = sum_r;
-      s_red[2 * W + warp] = sum_i;
+      s_red[0][warp] = sum_w;
+      s_red[1][warp] = sum_r;
+      s_red[2][warp] = sum_i;
     }
     __syncthreads();
-    if (warp == 0 && lane == 0)
-      for (int k = 1; k < W; ++k) {
-        sum_w += s_red[k];
-        sum_r += s_red[W + k];
-        sum_i += s_red[2 * W + k];
+    if (threadIdx.x < 3) {
+      float v = 0.0f;
+      for (int k = 0; k < W; ++k) v += s_red[threadIdx.x][k];
+      s_red[threadIdx.x][0] = v;
+    }
+    __syncthreads();
+    sum_w = s_red[0][0];
+    sum_r = s_red[1][0];
+    sum_i = s_red[2][0];
+    if constexpr (CL) {
+      if (threadIdx.x == 0)
+        for (int k = 0; k < 3; ++k)
+          cluster_put1(&s_sum[k][rank], 0, s_red[k][0]);
+      cluster_barrier();
+      if (rank == 0 && threadIdx.x == 0) {
+        sum_w = sum_r = sum_i = 0.0f;
+        for (int k = 0; k < split; ++k) {
+          sum_w += s_sum[0][k];
+          sum_r += s_sum[1][k];
+          sum_i += s_sum[2][k];
+        }
       }
+    }
   }
   if (lane == 0 && wr == 0) {
     if (p.part) {
@@ -717,14 +1057,35 @@ __global__ void __launch_bounds__(256) gated_step_kernel(const GatedStepArgs p) 
   const float rv = Elem<T>::load(static_cast<const T*>(p.r) + bt * p.r_sb + d * p.r_sd);
   const float iv = Elem<T>::load(static_cast<const T*>(p.i) + bt * p.i_sb + d * p.i_sd);
   const float zv = Z ? Elem<T>::load(static_cast<const T*>(p.z) + bt * p.z_sb + d * p.z_sd) : 0.0f;
-  const Gates g = gates<Z>(rv + w.rb, iv + w.ib, zv);
-  const Decay dc = decay(w.rate * g.r);
-  const float h = fmaf(dc.a, *st, sqrt_approx(dc.v) * (g.i * xv));
+  const f2_t x2[1] = {f2s(xv)}, r2[1] = {f2s(rv)}, i2[1] = {f2s(iv)};
+  f2_t z2[1] = {f2s(zv)};
+  float a[2], b[2];
+  steps<Z, true, 2>(x2, r2, i2, z2, w, a, b);  // a gate each: the step waits for memory, not for the SFU
+  const float h = fmaf(a[0], *st, b[0]);
   *st = h;
-  const float y = Z ? h * (zv * g.sz) : h;
+  const float y = Z ? h * f2lo(z2[0]) : h;
   T* o = static_cast<T*>(p.out) + bt * p.o_sb + d * p.o_sd;
   if constexpr (sizeof(T) == 2) *o = f_to_bf16(y);
   else *o = y;
+}
+
+// ---------------------------------------------------------------- launch
+
+template <typename K>
+cudaError_t gated_launch(K kernel, const GatedArgs& a, int warps, size_t smem, cudaStream_t s) {
+  const int64_t rows = int64_t(a.Bt) * a.D;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(unsigned(warps == 1 ? (rows + 3) / 4 : rows * a.split));
+  c.blockDim = dim3(unsigned(gated_threads(warps)));
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = unsigned(a.split);
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  c.attrs = at;
+  c.numAttrs = a.split > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&c, kernel, a);
 }
 
 }  // namespace mssm

@@ -196,6 +196,15 @@ def test_cpu_tensors_are_refused():
         m.w4_pack(torch.zeros(16, 32, dtype=torch.uint8), torch.zeros(16, 1), group_size=64)
 
 
+def test_plan_options(lib):  # noqa: F811
+    for opt, good, bad in ((9, (1, 4, 8, 0), (-1, 2, 16)), (10, (1, 2, 4, 8, 0), (-1, 3, 16))):
+        lib.mssm_set_option.argtypes = [ctypes.c_int, ctypes.c_int64]
+        for v in bad:
+            assert lib.mssm_set_option(opt, v) == INVALID
+        for v in good:
+            assert lib.mssm_set_option(opt, v) == 0
+
+
 def test_kernel_kinds(lib):  # noqa: F811
     """The kinds that mssm_kernel_stats fills stay five; the newer ones are counted by mssm_kernel_stats_all."""
     guard = (ctypes.c_int64 * 9)(*[77] * 9)

@@ -292,6 +292,39 @@ def test_strides_and_alignment(cuda_device, io, how):
     assert (cat[..., 0] == 5).all() and (cat[..., L + 1:] == 5).all()
 
 
+PLANS = [(1, 1), (4, 1), (8, 1), (8, 2), (8, 4), (8, 8)]
+
+
+@pytest.mark.parametrize("plan", PLANS)
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("L", [1, 300, 2049, 7001, 33000])
+def test_every_plan(cuda_device, plan, io, L):
+    """Every way of sharing a row among warps and CTAs, whatever the automatic choice is."""
+    import selective_state_space_46_b200 as m
+    try:
+        m.mssm_set_option(m.MSSM_OPT_GATED_WARPS, plan[0])
+        m.mssm_set_option(m.MSSM_OPT_GATED_SPLIT, plan[1])
+        p = ref.gated_inputs(2, 3, L, io, h0=True, seed=L)
+        check_fwd(p, io)
+        check_bwd(p, io, dlast=True)
+        cu = sorted({0, 1, L // 3, L // 2, L - 1, L}) + [L]
+        p = ref.gated_inputs(1, 3, L, io, h0=True, gate=False, cu=cu, seed=L + 1)
+        check_fwd(p, io)
+        check_bwd(p, io, dlast=True)
+    finally:
+        m.mssm_set_option(m.MSSM_OPT_GATED_WARPS, 0)
+        m.mssm_set_option(m.MSSM_OPT_GATED_SPLIT, 0)
+
+
+def test_many_sequences_in_a_window(cuda_device):
+    """More sequences than one look at the offsets takes, several in a thread's window."""
+    rng = np.random.default_rng(17)
+    cu = np.concatenate([[2], 2 + np.cumsum(rng.integers(0, 4, 900))])
+    p = ref.gated_inputs(1, 3, int(cu[-1]) + 5, "f32", h0=True, cu=cu, seed=18)
+    check_fwd(p, "f32")
+    check_bwd(p, "f32", dlast=True)
+
+
 def test_pieces_reproduce_the_whole(cuda_device):
     """A sequence processed in two pieces, the state handed on, and its gradient handed back."""
     import selective_state_space_46_b200 as m
