@@ -90,29 +90,38 @@ __device__ __forceinline__ float logistic_exact(float v) {
 // per-channel constants of a row
 struct GatedRow {
   float rate;    // c softplus(lam)
+  float root;    // sqrt(2 rate)
   float cr, ci;  // -log2(e) times the biases
   bool slow;     // some gate may take rate r past the series of the decay: CARE
 };
 
 constexpr float kSeriesEnd = 0.25f;
-constexpr float kVScale = 1048576.0f;  // 2^20
 
 template <typename Args>
 __device__ __forceinline__ GatedRow gated_row(const Args& p, int d) {
   GatedRow w;
   w.rate = p.c * softplus_exact(p.lam[d * p.lam_s]);
+  w.root = sqrtf(2.0f * w.rate);
   w.cr = p.rb ? -kLog2e * p.rb[d * p.rb_s] : 0.0f;
   w.ci = p.ib ? -kLog2e * p.ib[d * p.ib_s] : 0.0f;
   w.slow = !(w.rate < kSeriesEnd);
   return w;
 }
 
-// Gates of a pair of steps: sigmoid(v) = 1 / (1 + e), e = 2^(-log2(e) v).
-// The usual path (CARE = false) gives the recurrence gate its own reciprocal and lets the input gate and
-// sigmoid(z) share that of their product: 5 SFU results a step instead of 6.  `most` collects what has
-// to stay below 2^125 for it; where it does not, or is a NaN, the window is computed once more with CARE:
-// a reciprocal for each gate, so every gate falls to the smallest normal number before it is zero, and a
-// NaN stays with its own gate.  Rows of fast decays take CARE at once.
+// sigmoid(v) = 1 / p, p = 1 + 2^(-log2(e) v).
+//
+// The usual path (CARE = false) takes one reciprocal root for all gates of a step,
+//   u = 1 / (sqrt(pr) pi pz),  sqrt(r) = u pi pz,  sqrt(r) i = u pz,  1 / pz = (u pi)(pr sqrt(r)),
+// and none for sqrt(1 - a^2): with y = rate r, below y = 1/4,
+//   sqrt(1 - exp(-2y)) = sqrt(2 rate) sqrt(r) P(y),   P(y) = sqrt((1 - exp(-2y)) / (2y)),
+// a polynomial (its reciprocal R is another).  3 SFU results a step, 4 with z; a reciprocal each and two
+// roots would be 5 and 7, which is more than the I/O lets the SFU have (2.7 steps a cycle and SM of 10 bytes).
+// The polynomials are near-minimax fits on [0, 1/4], relative errors below 2^-27.
+//
+// `most` collects pr pi^2 pz^2, which has to stay below 2^125 for this; where it does not, or is a NaN, the
+// window is computed once more with CARE: a reciprocal for each gate, so every gate falls to the smallest
+// normal number before it is zero, and a NaN stays with its own gate.  Rows whose rate reaches 1/4 take
+// CARE at once.
 constexpr float kGateMost = 4.2535296e37f;  // 2^125
 
 __device__ __forceinline__ f2_t ex2_2(f2_t v) {
@@ -125,112 +134,64 @@ __device__ __forceinline__ f2_t rcp_2(f2_t v) {
   f2split(v, a, b);
   return f2(rcpf(a), rcpf(b));
 }
+__device__ __forceinline__ f2_t rsqrt_2(f2_t v) {
+  float a, b;
+  f2split(v, a, b);
+  return f2(rsqrt_approx(a), rsqrt_approx(b));
+}
+__device__ __forceinline__ f2_t one_plus(f2_t v) { return add2(v, f2s(1.0f)); }
 __device__ __forceinline__ void note_most(float& most, f2_t v) {
   float a, b;
   f2split(v, a, b);
   most = max_nan(most, max_nan(a, b));
 }
 
-template <bool Z, bool CARE>
-__device__ __forceinline__ void gate_pair(f2_t rr, f2_t ii, f2_t zz, const GatedRow& w, f2_t& r, f2_t& i, f2_t& sz,
-                                          float& most) {
-  r = rcp_2(add2(ex2_2(fma2(rr, f2s(-kLog2e), f2s(w.cr))), f2s(1.0f)));
-  const f2_t pi = add2(ex2_2(fma2(ii, f2s(-kLog2e), f2s(w.ci))), f2s(1.0f));
-  if constexpr (!Z) {
-    i = rcp_2(pi);
-  } else {
-    const f2_t pz = add2(ex2_2(mul2(zz, f2s(-kLog2e))), f2s(1.0f));
-    if constexpr (CARE) {
-      i = rcp_2(pi);
-      sz = rcp_2(pz);
-    } else {
-      const f2_t both = mul2(pi, pz), q = rcp_2(both);
-      note_most(most, both);
-      i = mul2(q, pz);
-      sz = mul2(q, pi);
-    }
-  }
-}
-
 // CARE: a sigmoid and its complement, which is 1 long before e / (1 + e) overflows
 __device__ __forceinline__ void sigmoid_both(f2_t v, f2_t& s, f2_t& c) {
   const f2_t e = ex2_2(v);
-  s = rcp_2(add2(e, f2s(1.0f)));
+  s = rcp_2(one_plus(e));
   const f2_t q = mul2(e, s);
   c = f2(f2lo(e) < 1.0e18f ? f2lo(q) : 1.0f, f2hi(e) < 1.0e18f ? f2hi(q) : 1.0f);
 }
 
-// The same with the complements 1 - r, 1 - i, 1 - sigmoid(z) = e / (1 + e), free of the cancellation of
-// 1 - r.
-template <bool Z, bool CARE>
-__device__ __forceinline__ void gate_pair_grad(f2_t rr, f2_t ii, f2_t zz, const GatedRow& w, f2_t& r, f2_t& i, f2_t& sz,
-                                               f2_t& rc, f2_t& ic, f2_t& szc, float& most) {
-  const f2_t ur = fma2(rr, f2s(-kLog2e), f2s(w.cr)), ui = fma2(ii, f2s(-kLog2e), f2s(w.ci));
-  if constexpr (CARE) {
-    sigmoid_both(ur, r, rc);
-    sigmoid_both(ui, i, ic);
-    if constexpr (Z) sigmoid_both(mul2(zz, f2s(-kLog2e)), sz, szc);
-  } else {
-    const f2_t er = ex2_2(ur), ei = ex2_2(ui);
-    const f2_t pr = add2(er, f2s(1.0f)), pi = add2(ei, f2s(1.0f));
-    r = rcp_2(pr);
-    rc = mul2(er, r);
-    note_most(most, pr);
-    if constexpr (Z) {
-      const f2_t ez = ex2_2(mul2(zz, f2s(-kLog2e))), pz = add2(ez, f2s(1.0f));
-      const f2_t both = mul2(pi, pz), q = rcp_2(both);
-      note_most(most, both);
-      i = mul2(q, pz);
-      sz = mul2(q, pi);
-      szc = mul2(ez, sz);
-    } else {
-      note_most(most, pi);
-      i = rcp_2(pi);
-    }
-    ic = mul2(ei, i);
-  }
-}
-
-// The decay a = exp(-y), y = rate r >= 0, and v = 2^20 (1 - a^2).  Below y = 1/4, m = 1 - a is the Taylor series
-// y (1 - y/2 + ... - y^5/720) (first omitted term y^6/5040 < 5e-8 of it), so a is rounded once: a
-// relative error e of a slow decay compounds over its memory to e / y, and the SFU's 2^-22 would be
-// felt.  v = 2^20 m (1 + a) keeps the series' relative accuracy.  Above 1/4, m >= 0.22 and the SFU
-// exponential serves both; only rows whose rate reaches 1/4 (which take CARE) look.
-template <bool CARE>
-__device__ __forceinline__ void decay_pair(f2_t y, f2_t& a, f2_t& v) {
-  f2_t q = fma2(y, f2s(-1.0f / 720.0f), f2s(1.0f / 120.0f));
-  q = fma2(y, q, f2s(-1.0f / 24.0f));
-  q = fma2(y, q, f2s(1.0f / 6.0f));
-  q = fma2(y, q, f2s(-0.5f));
+// 1 - exp(-y), y < 1/4.  With a = 1 minus it, a is rounded once: a relative error e of a slow decay compounds
+// over its memory to e / y, and the SFU exponential's 2^-22 would be felt.
+__device__ __forceinline__ f2_t decay_loss(f2_t y) {
+  f2_t q = fma2(y, f2s(0.00753015606f), f2s(-0.0415001251f));
+  q = fma2(y, q, f2s(0.166652888f));
+  q = fma2(y, q, f2s(-0.499999642f));
   q = fma2(y, q, f2s(1.0f));
-  f2_t m = mul2(y, q);
-  a = fma2(m, f2s(-1.0f), f2s(1.0f));
-  if constexpr (CARE) {
-    float y0, y1, m0, m1, a0, a1;
-    f2split(y, y0, y1);
-    f2split(m, m0, m1);
-    f2split(a, a0, a1);
-    const float e0 = ex2f(-kLog2e * y0), e1 = ex2f(-kLog2e * y1);
-    m = f2(y0 < kSeriesEnd ? m0 : 1.0f - e0, y1 < kSeriesEnd ? m1 : 1.0f - e1);
-    a = f2(y0 < kSeriesEnd ? a0 : e0, y1 < kSeriesEnd ? a1 : e1);
-  }
-  v = mul2(m, fma2(a, f2s(kVScale), f2s(kVScale)));
+  return mul2(y, q);
+}
+__device__ __forceinline__ f2_t root_series(f2_t y) {  // P
+  f2_t q = fma2(y, f2s(0.0123667913f), f2s(-0.0622208975f));
+  q = fma2(y, q, f2s(0.208310276f));
+  q = fma2(y, q, f2s(-0.499999404f));
+  return fma2(y, q, f2s(1.0f));
+}
+__device__ __forceinline__ f2_t root_inverse(f2_t y) {  // R
+  f2_t q = fma2(y, f2s(-0.000555377337f), f2s(-0.0210434105f));
+  q = fma2(y, q, f2s(0.041683875f));
+  q = fma2(y, q, f2s(0.499999553f));
+  return fma2(y, q, f2s(1.0f));
 }
 
-// 2^-20 / sqrt(1 - a^2), so that v times it is sqrt(1 - a^2); finite at v = 0.  The smallest normal number is
-// added to 2^20 v = 2^40 (1 - a^2), where it changes no normal 1 - a^2.
-__device__ __forceinline__ f2_t rsqrt_pair(f2_t v) {
-  float v0, v1;
-  f2split(fma2(v, f2s(kVScale), f2s(1.17549435e-38f)), v0, v1);
-  return f2(rsqrt_approx(v0), rsqrt_approx(v1));
-}
+// CARE: a, sqrt(1 - a^2) and y / sqrt(1 - a^2) for any y.  Above 1/4, 1 - a >= 0.22 and the SFU exponential
+// serves.  1 - a^2 = (1 - a)(1 + a) is scaled by 2^40 (v: 2^20) so that the smallest normal number, added
+// for a finite root of 0, changes no normal 1 - a^2.
+constexpr float kVScale = 1048576.0f;  // 2^20
 
-// zeros the steps of a window that `valid` leaves out
-template <int E>
-__device__ __forceinline__ void blank(f2_t (&v)[E / 2], unsigned valid) {
-#pragma unroll
-  for (int k = 0; k < E / 2; ++k)
-    v[k] = f2(valid >> (2 * k) & 1u ? f2lo(v[k]) : 0.0f, valid >> (2 * k + 1) & 1u ? f2hi(v[k]) : 0.0f);
+__device__ __forceinline__ void decay_care(f2_t y, f2_t& a, f2_t& beta, f2_t& y_beta) {
+  float y0, y1, m0, m1;
+  f2split(y, y0, y1);
+  f2split(decay_loss(y), m0, m1);
+  const float e0 = ex2f(-kLog2e * y0), e1 = ex2f(-kLog2e * y1);
+  const f2_t m = f2(y0 < kSeriesEnd ? m0 : 1.0f - e0, y1 < kSeriesEnd ? m1 : 1.0f - e1);
+  a = f2(y0 < kSeriesEnd ? 1.0f - m0 : e0, y1 < kSeriesEnd ? 1.0f - m1 : e1);
+  const f2_t v = mul2(m, fma2(a, f2s(kVScale), f2s(kVScale)));
+  const f2_t q = rsqrt_2(fma2(v, f2s(kVScale), f2s(1.17549435e-38f)));
+  beta = mul2(v, q);
+  y_beta = mul2(mul2(y, f2s(kVScale)), q);
 }
 
 // A window's a, driven terms b = sqrt(1 - a^2) i x and, with Z, silu(z) (in zz).  Returns `most`.
@@ -240,15 +201,37 @@ __device__ __forceinline__ float steps(const f2_t (&x)[E / 2], const f2_t (&rr)[
   float most = 0.0f;
 #pragma unroll
   for (int k = 0; k < E / 2; ++k) {
-    f2_t r, i, sz, a, v;
-    gate_pair<Z, CARE>(rr[k], ii[k], zz[k], w, r, i, sz, most);
-    decay_pair<CARE>(mul2(r, f2s(w.rate)), a, v);
-    const f2_t b = mul2(mul2(mul2(v, rsqrt_pair(v)), i), x[k]);
+    const f2_t pr = one_plus(ex2_2(fma2(rr[k], f2s(-kLog2e), f2s(w.cr))));
+    const f2_t pi = one_plus(ex2_2(fma2(ii[k], f2s(-kLog2e), f2s(w.ci))));
+    const f2_t pz = Z ? one_plus(ex2_2(mul2(zz[k], f2s(-kLog2e)))) : 0;
+    f2_t a, b;
+    if constexpr (CARE) {
+      f2_t beta, unused;
+      decay_care(mul2(rcp_2(pr), f2s(w.rate)), a, beta, unused);
+      b = mul2(mul2(beta, rcp_2(pi)), x[k]);
+      if (Z) zz[k] = mul2(zz[k], rcp_2(pz));
+    } else {
+      const f2_t t = Z ? mul2(pi, pz) : pi;
+      const f2_t all = mul2(mul2(pr, t), t);
+      note_most(most, all);
+      const f2_t u = rsqrt_2(all), s = mul2(u, t);
+      const f2_t y = mul2(mul2(s, s), f2s(w.rate));
+      a = fma2(decay_loss(y), f2s(-1.0f), f2s(1.0f));
+      b = mul2(mul2(mul2(Z ? mul2(u, pz) : u, f2s(w.root)), root_series(y)), x[k]);
+      if (Z) zz[k] = mul2(mul2(mul2(u, pi), mul2(pr, s)), zz[k]);
+    }
     f2split(a, av[2 * k], av[2 * k + 1]);
     f2split(b, bv[2 * k], bv[2 * k + 1]);
-    if (Z) zz[k] = mul2(zz[k], sz);
   }
   return most;
+}
+
+// zeros the steps of a window that `valid` leaves out
+template <int E>
+__device__ __forceinline__ void blank(f2_t (&v)[E / 2], unsigned valid) {
+#pragma unroll
+  for (int k = 0; k < E / 2; ++k)
+    v[k] = f2(valid >> (2 * k) & 1u ? f2lo(v[k]) : 0.0f, valid >> (2 * k + 1) & 1u ? f2hi(v[k]) : 0.0f);
 }
 
 // The same for the backward pass.  In: x, r, i, z, dout.  Out: y = rate r (x), 1 - r (r), i x rho (i),
@@ -261,21 +244,48 @@ __device__ __forceinline__ float steps_grad(f2_t (&xv)[E / 2], f2_t (&rv)[E / 2]
   float most = 0.0f;
 #pragma unroll
   for (int k = 0; k < E / 2; ++k) {
-    f2_t rg, ig, sz = 0, rc, ic, szc = 0, a, v;
-    gate_pair_grad<Z, CARE>(rv[k], iv[k], Z ? zv[k] : 0, w, rg, ig, sz, rc, ic, szc, most);
-    f2_t y = mul2(rg, f2s(w.rate));
-    if (!whole) {
+    const f2_t ur = fma2(rv[k], f2s(-kLog2e), f2s(w.cr)), ui = fma2(iv[k], f2s(-kLog2e), f2s(w.ci));
+    const f2_t uz = Z ? mul2(zv[k], f2s(-kLog2e)) : 0;
+    f2_t y, ic, sz = 0, szc = 0, a;
+    auto only_valid = [&] {
+      if (whole) return;
       f2_t one[1] = {y};
       blank<2>(one, valid >> (2 * k));
       y = one[0];
+    };
+    if constexpr (CARE) {
+      f2_t r, i, beta, y_beta;
+      sigmoid_both(ur, r, rv[k]);
+      sigmoid_both(ui, i, ic);
+      if (Z) sigmoid_both(uz, sz, szc);
+      y = mul2(r, f2s(w.rate));
+      only_valid();
+      decay_care(y, a, beta, y_beta);
+      pv[k] = mul2(beta, i);
+      iv[k] = mul2(mul2(i, xv[k]), mul2(a, y_beta));
+    } else {
+      const f2_t er = ex2_2(ur), ei = ex2_2(ui), ez = Z ? ex2_2(uz) : 0;
+      const f2_t pr = one_plus(er), pi = one_plus(ei), pz = Z ? one_plus(ez) : 0;
+      const f2_t t = Z ? mul2(pi, pz) : pi;
+      const f2_t all = mul2(mul2(pr, t), t);
+      note_most(most, all);
+      const f2_t u = rsqrt_2(all), s = mul2(u, t), r = mul2(s, s), sp = mul2(pr, s);  // sp = 1 / s
+      const f2_t si = Z ? mul2(u, pz) : u;                                             // sqrt(r) i
+      ic = mul2(ei, mul2(si, sp));
+      if (Z) {
+        sz = mul2(mul2(u, pi), sp);
+        szc = mul2(ez, sz);
+      }
+      rv[k] = mul2(er, r);
+      y = mul2(r, f2s(w.rate));
+      only_valid();
+      a = fma2(decay_loss(y), f2s(-1.0f), f2s(1.0f));
+      const f2_t g = mul2(si, f2s(w.root));
+      pv[k] = mul2(g, root_series(y));
+      iv[k] = mul2(mul2(mul2(g, f2s(0.5f)), xv[k]), mul2(a, root_inverse(y)));
     }
-    decay_pair<CARE>(y, a, v);
-    const f2_t q = rsqrt_pair(v);
-    pv[k] = mul2(mul2(v, q), ig);
     const f2_t b = mul2(pv[k], xv[k]);
-    iv[k] = mul2(mul2(ig, xv[k]), mul2(a, mul2(mul2(y, f2s(kVScale)), q)));
     xv[k] = y;
-    rv[k] = rc;
     cv[k] = mul2(b, ic);
     if (Z) {
       const f2_t ds = mul2(gv[k], sz);
@@ -383,80 +393,93 @@ __device__ __forceinline__ unsigned misalign(const T* p) {
 
 // ---------------------------------------------------------------- packed sequences
 
-// What a window holds of the packed sequences: bit j for step t0 + j.
-struct SeqMask {
-  unsigned valid, first, last;  // inside a sequence; its first step; its last step
-};
-
-// The largest j in [lo, S] with cu[j] <= t, as a sequence: in [0, S) whatever the offsets hold.
-__device__ __forceinline__ int seq_of(const int* cu, int S, int t, int lo) {
-  int hi = S + 1;
+// The largest j in [0, S) with cu[j] <= t (0 if there is none), whatever the offsets hold.
+__device__ __forceinline__ int seq_of(const int* cu, int S, int t) {
+  int lo = 0, hi = S + 1;
   while (lo < hi) {
     const int mid = lo + (hi - lo) / 2;
     if (__ldg(cu + mid) <= t) lo = mid + 1;
     else hi = mid;
   }
-  const int j = lo - 1;
-  return j < 0 ? 0 : j < S ? j : S - 1;
+  return max(min(lo - 1, S - 1), 0);
 }
 
-// A warp's walk through the offsets: `before` counts those below the warp's first step, 32 looked at
-// together.  Offsets that are out of order give wrong counts in [0, S + 1] and an end to every loop.
+// What a window holds of the packed sequences: bit j for step t0 + j.
+struct SeqMask {
+  unsigned valid, first, last;  // inside a sequence; its first step; its last step
+  unsigned offs;                // steps with an offset
+  int below;                    // offsets before t0
+  bool twice;                   // some step has more than one offset (an empty sequence)
+};
+
+// A warp's walk through the offsets, 32 of them in its lanes.  Offsets that are out of order give wrong
+// sequences in [0, S) and an end to every loop.
 struct SeqWalk {
   const int* cu;
   int S, c0, cS;  // the first and last offset
-  int before;
+  int base, v;    // the lane's offset is number base + lane
 
-  __device__ __forceinline__ void start(const int* offsets, int n) {
+  __device__ __forceinline__ int get(int j) const { return j <= S ? __ldg(cu + j) : 0x7fffffff; }
+  __device__ __forceinline__ void start(const int* offsets, int n, int lane) {
     cu = offsets;
     S = n;
     c0 = __ldg(cu);
     cS = __ldg(cu + n);
-    before = 0;
+    base = 0;
+    v = get(lane);
   }
-  // To the warp's steps [wt, wt + n): counts the offsets below it and says whether it lies inside one
-  // sequence, with no first or last step (up = false: the walk goes back, by bisection).
-  __device__ __forceinline__ bool enter(int wt, int n, int lane, bool up) {
-    if (!up) {
-      int lo = 0;
-      while (lo < before) {
-        const int mid = lo + (before - lo) / 2;
-        if (__ldg(cu + mid) < wt) lo = mid + 1;
-        else before = mid;
-      }
+  // To the warp's steps [wt, wt + n), up or down the row.  Says whether they lie inside one sequence, with no
+  // first or last step.
+  __device__ __forceinline__ bool enter(int wt, int n, int lane) {
+    unsigned below = __ballot_sync(~0u, v < wt);
+    while (below == ~0u) {
+      base += 32;
+      v = get(base + lane);
+      below = __ballot_sync(~0u, v < wt);
     }
-    int v;
-    while (true) {
-      v = before + lane <= S ? __ldg(cu + before + lane) : 0x7fffffff;
-      const unsigned below = __ballot_sync(~0u, v < wt);
-      before += __popc(below);
-      if (below != ~0u) break;
+    while (below == 0u && base > 0) {
+      base -= 32;
+      v = get(base + lane);
+      below = __ballot_sync(~0u, v < wt);
+      if (below == ~0u) break;
     }
-    return !__any_sync(~0u, v >= wt && v <= wt + n) && before >= 1 && before <= S;
+    const int before = base + __popc(below);
+    return !__any_sync(~0u, v >= wt && v <= wt + n) && below != ~0u && before >= 1 && before <= S;
   }
   template <int E>
   __device__ __forceinline__ SeqMask masks(int wt, int t0, int L, int lane) const {
-    SeqMask m{0u, 0u, 0u};
+    SeqMask m{0u, 0u, 0u, 0u, 0, false};
     constexpr unsigned kAll = (1u << E) - 1u;
     const int lo = max(max(c0, 0) - t0, 0), hi = min(min(cS, L) - t0, E);
     if (hi > lo) m.valid = (kAll >> (E - hi)) & ~((1u << lo) - 1u);
     const int te = wt + 32 * E;
-    for (int at = before;; at += 32) {
-      const int v = at + lane <= S ? __ldg(cu + at + lane) : 0x7fffffff;
-      unsigned in = __ballot_sync(~0u, v >= wt && v <= te);
+    m.below = base + __popc(__ballot_sync(~0u, v < wt));
+    int o32 = v;
+    for (int at = base;;) {
+      unsigned in = __ballot_sync(~0u, o32 >= wt && o32 <= te);
       while (in) {
-        const int o = __shfl_sync(~0u, v, __ffs(in) - 1) - t0;
+        const int o = __shfl_sync(~0u, o32, __ffs(in) - 1) - t0;
         in &= in - 1;
-        if (o >= 0 && o < E) m.first |= 1u << o;
+        if (o < 0) ++m.below;
+        if (o >= 0 && o < E) {
+          m.twice |= m.offs >> o & 1u;
+          m.offs |= 1u << o;
+        }
         if (o >= 1 && o <= E) m.last |= 1u << (o - 1);
       }
-      if (__any_sync(~0u, v > te)) break;
+      if (__any_sync(~0u, o32 > te)) break;
+      at += 32;
+      o32 = get(at + lane);
     }
-    m.first &= m.valid;
+    m.first = m.offs & m.valid;
     m.last &= m.valid;
     return m;
   }
-  __device__ __forceinline__ int seq(int t) const { return seq_of(cu, S, t, before > 0 ? before - 1 : 0); }
+  // the sequence of step t0 + k
+  __device__ __forceinline__ int seq(const SeqMask& m, int t0, int k) const {
+    if (m.twice) return seq_of(cu, S, t0 + k);
+    return max(min(m.below + __popc(m.offs & ((2u << k) - 1u)) - 1, S - 1), 0);
+  }
 };
 
 // ---------------------------------------------------------------- composing affine maps
@@ -615,8 +638,6 @@ __global__ void __launch_bounds__(gated_threads(W)) gated_scan_kernel(const Gate
   const T* i = static_cast<const T*>(p.i) + bt * p.i_sb + d * p.i_sd;
   const T* z = Z ? static_cast<const T*>(p.z) + bt * p.z_sb + d * p.z_sd : nullptr;
   T* out = static_cast<T*>(p.out) + bt * p.o_sb + d * p.o_sd;
-  const GatedRow w = gated_row(p, d);
-  if (CL) cluster_barrier();  // every CTA's shared memory is there
   // windows start on 16-byte boundaries when every tensor's row is equally far from one
   const unsigned mis = misalign(x);
   const bool vec = misalign(r) == mis && misalign(i) == mis && misalign(out) == mis && (!Z || misalign(z) == mis);
@@ -625,7 +646,7 @@ __global__ void __launch_bounds__(gated_threads(W)) gated_scan_kernel(const Gate
   if (!VL && p.h0) h = p.h0[bt * p.h0_sb + d * p.h0_sd];
   SeqWalk walk;
   if (VL) {
-    walk.start(p.cu, p.S);
+    walk.start(p.cu, p.S, lane);
     if (p.last)
       for (int j = wr * 32 + lane; j < p.S; j += 32 * W * split)
         if (p.cu[j] >= p.cu[j + 1])
@@ -642,16 +663,20 @@ __global__ void __launch_bounds__(gated_threads(W)) gated_scan_kernel(const Gate
     if (Z) nx.z = win_load<T, E>(z, t, p.L, vec);
   };
   fetch(wt + lane * E);
+  const GatedRow w = gated_row(p, d);
+  if (CL) cluster_barrier();  // every CTA's shared memory is there
   for (int base = -off; base < p.L; base += tile, wt += tile) {
     const int t0 = wt + lane * E;
     f2_t xv[E / 2], rv[E / 2], iv[E / 2], zv[E / 2];
-    SeqMask m{(1u << E) - 1u, 0u, 0u};
+    SeqMask m{(1u << E) - 1u, 0u, 0u, 0u, 0, false};
     bool whole = wt >= 0 && wt + 32 * E <= p.L;
-    if (VL) whole = walk.enter(wt, 32 * E, lane, true) && whole;
+    if (VL) whole = walk.enter(wt, 32 * E, lane) && whole;
     if (!whole) {
       if (VL) m = walk.template masks<E>(wt, t0, p.L, lane);
       else m.valid = row_mask<E>(t0, p.L);
     }
+    float h0_first = 0.0f;  // of the window's first sequence start, asked for early
+    if (VL && m.first && p.h0) h0_first = p.h0[int64_t(walk.seq(m, t0, __ffs(m.first) - 1)) * p.h0_sb + d * p.h0_sd];
     auto unpack = [&] {
       win_get(nx.x, xv);
       win_get(nx.r, rv);
@@ -687,7 +712,10 @@ __global__ void __launch_bounds__(gated_threads(W)) gated_scan_kernel(const Gate
       for (int k = 0; k < E; ++k) {
         if (!(m.valid >> k & 1u)) av[k] = 1.0f, bv[k] = 0.0f;
         if (VL && (m.first >> k & 1u)) {
-          if (p.h0) bv[k] = fmaf(av[k], p.h0[int64_t(walk.seq(t0 + k)) * p.h0_sb + d * p.h0_sd], bv[k]);
+          if (p.h0) {
+            const bool early = (m.first & ((1u << k) - 1u)) == 0u;
+            bv[k] = fmaf(av[k], early ? h0_first : p.h0[int64_t(walk.seq(m, t0, k)) * p.h0_sb + d * p.h0_sd], bv[k]);
+          }
           av[k] = kResetA;
         }
         float ca = av[k], cb = bv[k];
@@ -713,7 +741,7 @@ __global__ void __launch_bounds__(gated_threads(W)) gated_scan_kernel(const Gate
         for (int q = 0; q < 2; ++q) {
           const int e = 2 * k + q;
           hk = apply<VL>(av[e], bv[e], hk);
-          if ((m.last >> e & 1u) && p.last) p.last[int64_t(walk.seq(t0 + e)) * p.ls_sb + d * p.ls_sd] = hk;
+          if ((m.last >> e & 1u) && p.last) p.last[int64_t(walk.seq(m, t0, e)) * p.ls_sb + d * p.ls_sd] = hk;
           o[q] = hk;
         }
         ov[k] = Z ? mul2(f2(o[0], o[1]), zv[k]) : f2(o[0], o[1]);
@@ -760,15 +788,13 @@ __global__ void __launch_bounds__(gated_threads(W)) gated_bwd_kernel(const Gated
   T* dr = static_cast<T*>(p.dr) + bt * p.dr_sb + d * p.dr_sd;
   T* di = static_cast<T*>(p.di) + bt * p.di_sb + d * p.di_sd;
   T* dz = Z ? static_cast<T*>(p.dz) + bt * p.dz_sb + d * p.dz_sd : nullptr;
-  const GatedRow w = gated_row(p, d);
-  if (CL) cluster_barrier();
   const unsigned mis = misalign(x);
   const bool vec = misalign(r) == mis && misalign(i) == mis && misalign(gy) == mis && misalign(dx) == mis &&
                    misalign(dr) == mis && misalign(di) == mis && (!Z || (misalign(z) == mis && misalign(dz) == mis));
   const int off = vec ? int(mis / sizeof(T)) : 0;
   SeqWalk walk;
   if (VL) {
-    walk.start(p.cu, p.S);
+    walk.start(p.cu, p.S, lane);
     if (p.dh0)
       for (int j = wr * 32 + lane; j < p.S; j += 32 * W * split)
         if (p.cu[j] >= p.cu[j + 1])
@@ -779,6 +805,7 @@ __global__ void __launch_bounds__(gated_threads(W)) gated_bwd_kernel(const Gated
   const int lane0 = wr * 32 * E - off;  // the warp's first step in the first tile
   int flip = 0;
 
+  GatedRow w;
   // forward sweep: the state before every tile
   float h = !VL && p.h0 ? p.h0[bt * p.h0_sb + d * p.h0_sd] : 0.0f;
   {
@@ -789,21 +816,44 @@ __global__ void __launch_bounds__(gated_threads(W)) gated_bwd_kernel(const Gated
       nx.i = win_load<T, E>(i, t, p.L, vec);
     };
     if (ntiles > 1) fetch(lane0 + lane * E);
+    w = gated_row(p, d);
+    if (CL) cluster_barrier();  // every CTA's shared memory is there
     for (int tl = 0; tl + 1 < ntiles; ++tl) {
       if (lane == 0 && wc == 0) ckpt[tl] = h;
       const int wt = lane0 + tl * tile, t0 = wt + lane * E;
       f2_t xv[E / 2], rv[E / 2], iv[E / 2];
-      win_get(nx.x, xv);
-      win_get(nx.r, rv);
-      win_get(nx.i, iv);
+      SeqMask m{(1u << E) - 1u, 0u, 0u, 0u, 0, false};
+      bool whole = wt >= 0;  // only the last tile reaches the row's end
+      if (VL) whole = walk.enter(wt, 32 * E, lane) && whole;
+      if (!whole) {
+        if (VL) m = walk.template masks<E>(wt, t0, p.L, lane);
+        else m.valid = row_mask<E>(t0, p.L);
+      }
+      float h0_first = 0.0f;
+      if (VL && m.first && p.h0) h0_first = p.h0[int64_t(walk.seq(m, t0, __ffs(m.first) - 1)) * p.h0_sb + d * p.h0_sd];
+      auto unpack = [&] {
+        win_get(nx.x, xv);
+        win_get(nx.r, rv);
+        win_get(nx.i, iv);
+        if (!whole) {
+          blank<E>(xv, m.valid);
+          blank<E>(rv, m.valid);
+          blank<E>(iv, m.valid);
+        }
+      };
+      unpack();
       if (tl + 2 < ntiles) fetch(t0 + tile);
       float av[E], bv[E];
       float A = 1.0f, B = 0.0f;
-      bool whole = wt >= 0;  // only the last tile reaches the row's end
-      if (VL) whole = walk.enter(wt, 32 * E, lane, true) && whole;
       f2_t none[E / 2];
-      if (w.slow) steps<false, true, E>(xv, rv, iv, none, w, av, bv);
-      else steps<false, false, E>(xv, rv, iv, none, w, av, bv);
+      if (w.slow) {
+        steps<false, true, E>(xv, rv, iv, none, w, av, bv);
+      } else if (!(steps<false, false, E>(xv, rv, iv, none, w, av, bv) < kGateMost)) {
+        fetch(t0);
+        unpack();
+        if (tl + 2 < ntiles) fetch(t0 + tile);
+        steps<false, true, E>(xv, rv, iv, none, w, av, bv);
+      }
       if (whole) {
 #pragma unroll
         for (int k = 0; k < E; ++k) {
@@ -811,14 +861,14 @@ __global__ void __launch_bounds__(gated_threads(W)) gated_bwd_kernel(const Gated
           A *= av[k];
         }
       } else {
-        SeqMask m{0u, 0u, 0u};
-        if (VL) m = walk.template masks<E>(wt, t0, p.L, lane);
-        else m.valid = row_mask<E>(t0, p.L);
 #pragma unroll
         for (int k = 0; k < E; ++k) {
           if (!(m.valid >> k & 1u)) av[k] = 1.0f, bv[k] = 0.0f;
           if (VL && (m.first >> k & 1u)) {
-            if (p.h0) bv[k] = fmaf(av[k], p.h0[int64_t(walk.seq(t0 + k)) * p.h0_sb + d * p.h0_sd], bv[k]);
+            if (p.h0) {
+            const bool early = (m.first & ((1u << k) - 1u)) == 0u;
+            bv[k] = fmaf(av[k], early ? h0_first : p.h0[int64_t(walk.seq(m, t0, k)) * p.h0_sb + d * p.h0_sd], bv[k]);
+          }
             av[k] = kResetA;
           }
           float ca = av[k], cb = bv[k];
@@ -850,13 +900,15 @@ __global__ void __launch_bounds__(gated_threads(W)) gated_bwd_kernel(const Gated
   for (int tl = ntiles - 1; tl >= 0; --tl) {
     const int wt = lane0 + tl * tile, t0 = wt + lane * E;
     f2_t xv[E / 2], rv[E / 2], iv[E / 2], zv[E / 2], gv[E / 2];
-    SeqMask m{(1u << E) - 1u, 0u, 0u};
+    SeqMask m{(1u << E) - 1u, 0u, 0u, 0u, 0, false};
     bool whole = wt >= 0 && wt + 32 * E <= p.L;
-    if (VL) whole = walk.enter(wt, 32 * E, lane, false) && whole;
+    if (VL) whole = walk.enter(wt, 32 * E, lane) && whole;
     if (!whole) {
       if (VL) m = walk.template masks<E>(wt, t0, p.L, lane);
       else m.valid = row_mask<E>(t0, p.L);
     }
+    float h0_first = 0.0f;  // of the window's first sequence start, asked for early
+    if (VL && m.first && p.h0) h0_first = p.h0[int64_t(walk.seq(m, t0, __ffs(m.first) - 1)) * p.h0_sb + d * p.h0_sd];
     auto unpack = [&] {
       win_get(nx.x, xv);
       win_get(nx.r, rv);
@@ -871,6 +923,8 @@ __global__ void __launch_bounds__(gated_threads(W)) gated_bwd_kernel(const Gated
         if (Z) blank<E>(zv, m.valid);
       }
     };
+    float dl_last = 0.0f;  // of the window's last sequence end
+    if (VL && m.last && p.dlast) dl_last = p.dlast[int64_t(walk.seq(m, t0, 31 - __clz(m.last))) * p.dl_sb + d * p.dl_sd];
     unpack();
     if (tl > 0) fetch(t0 - tile);
     float av[E], bv[E];
@@ -917,7 +971,10 @@ __global__ void __launch_bounds__(gated_threads(W)) gated_bwd_kernel(const Gated
         hb[k] = 0.0f;
         float ca = av[k], cb = bv[k];
         if (m.first >> k & 1u) {
-          if (p.h0) hb[k] = p.h0[int64_t(walk.seq(t0 + k)) * p.h0_sb + d * p.h0_sd];
+          if (p.h0) {
+            const bool early = (m.first & ((1u << k) - 1u)) == 0u;
+            hb[k] = early ? h0_first : p.h0[int64_t(walk.seq(m, t0, k)) * p.h0_sb + d * p.h0_sd];
+          }
           cb = fmaf(ca, hb[k], cb);
           ca = kResetA;
         }
@@ -946,7 +1003,8 @@ __global__ void __launch_bounds__(gated_threads(W)) gated_bwd_kernel(const Gated
         float g = k & 1 ? f2hi(gv[k / 2]) : f2lo(gv[k / 2]);
         const bool end = m.last >> k & 1u;
         if (end && p.dlast) {
-          g += p.dlast[int64_t(walk.seq(t0 + k)) * p.dl_sb + d * p.dl_sd];
+          const bool early = (m.last >> k) == 1u;
+          g += early ? dl_last : p.dlast[int64_t(walk.seq(m, t0, k)) * p.dl_sb + d * p.dl_sd];
           gv[k / 2] = k & 1 ? f2(f2lo(gv[k / 2]), g) : f2(g, f2hi(gv[k / 2]));
         }
         float ca = end ? kResetA : av[k], cb = av[k] * g;
@@ -963,7 +1021,7 @@ __global__ void __launch_bounds__(gated_threads(W)) gated_bwd_kernel(const Gated
       sv[k] = VL && (m.last >> k & 1u) ? g : g + ck;
       ck = av[k] * sv[k];
       if (VL && (m.first >> k & 1u) && p.dh0)
-        p.dh0[int64_t(walk.seq(t0 + k)) * p.dh_sb + d * p.dh_sd] = ck;
+        p.dh0[int64_t(walk.seq(m, t0, k)) * p.dh_sb + d * p.dh_sd] = ck;
       if (VL && !whole && !(m.valid >> k & 1u)) sv[k] = 0.0f;  // what flows past the steps outside stays out of the sums
     }
     f2_t acc_w = 0, acc_r = 0, acc_i = 0;
