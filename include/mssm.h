@@ -466,7 +466,7 @@ mssm_status mssm_get_error(void *stream);
  *     the first gives up its bounded wait (about 0.5 s), runs from a zero state
  *     and sets the device error word; mssm_get_error then reports
  *     MSSM_ERR_TIMEOUT.  No fault, trap or unbounded wait is involved.
- *   MSSM_OPT_GATED_WARPS (value 0, 1, 4 or 8): warps of a CTA that share a row of the
+ *   MSSM_OPT_GATED_WARPS (value 0, 1, 2, 4 or 8): warps of a CTA that share a row of the
  *     gated scans; 0 automatic.
  *   MSSM_OPT_GATED_SPLIT (value 0, 1, 2, 4 or 8): CTAs (a cluster, of 8 warps each) that
  *     share a row of the gated scans; 0 automatic.

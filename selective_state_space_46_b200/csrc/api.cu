@@ -381,8 +381,8 @@ mssm_status mssm_set_option(int option, int64_t value) {
       g_decode_path = int(value);
       return MSSM_OK;
     case MSSM_OPT_GATED_WARPS:
-      if (value != 0 && value != 1 && value != 4 && value != 8)
-        return fail(MSSM_ERR_INVALID_ARG, "GATED_WARPS takes 0, 1, 4 or 8");
+      if (value != 0 && value != 1 && value != 2 && value != 4 && value != 8)
+        return fail(MSSM_ERR_INVALID_ARG, "GATED_WARPS takes 0, 1, 2, 4 or 8");
       g_gated_warps = int(value);
       return MSSM_OK;
     case MSSM_OPT_GATED_SPLIT:
@@ -1262,18 +1262,24 @@ mssm_status gated_prepare(const mssm_tensor* x, const mssm_tensor* r, const mssm
   return MSSM_OK;
 }
 
-// Warps of a CTA and CTAs that share a row of the gated scans.  Rows that fill the GPU with one warp each
-// need no barriers; fewer rows take 4 or 8 warps, and still fewer the CTAs of a cluster, as far as the
-// length gives each its steps.
+// Warps of a CTA and CTAs (a cluster) that share a row of the gated scans, from measurements of every plan
+// on 1 to 40960 rows (device us, bf16, forward / backward):
+//  * as many warps as keep all rows' warps within 70 per SM (three rounds of resident CTAs): 5120x4096
+//    with 1 / 2 / 4 / 8 warps 55 / 51 / 51 / 61 and 131 / 115 / 115 / 133, 1536x16384 76 / 68 / 61 / 66 and
+//    184 / 162 / 143 / 154, 300x32768 104 / 64 / 41 / 39; and no more than the length fills (8192x256: 14 / 23 / 37 / 76);
+//  * a cluster only while its CTAs' warps stay within 14 per SM and each keeps two tiles or more: 16x131072 in
+//    1 / 2 / 4 / 8 CTAs 68 / 68 / 37 / 25, 64x65536 37 / 39 / 25 / 27, but 148x65536 39 / 45 / 49 / 49.
 struct GatedShape {
   int warps, split;
 };
 
 GatedShape gated_shape(int64_t rows, int64_t L, int sms) {
-  const int64_t want = int64_t(sms) * 24, step = 32 * mssm::kGs;  // warps to fill the GPU, steps of a warp
+  const int64_t step = 32 * mssm::kGs;  // steps of a warp
   GatedShape g{1, 1};
-  if (L > step && rows < want) g.warps = L > 4 * step && rows * 4 < want ? 8 : 4;
-  while (g.warps == 8 && g.split < mssm::kMaxSplit && rows * 8 * g.split < want && L > 8 * step * g.split) g.split *= 2;
+  while (g.warps < 8 && g.warps * step < L && rows * g.warps * 2 <= int64_t(70) * sms) g.warps *= 2;
+  while (g.warps == 8 && g.split < mssm::kMaxSplit && rows * 8 * g.split * 2 <= int64_t(14) * sms &&
+         L >= 8 * step * 4 * g.split)
+    g.split *= 2;
   if (g_gated_warps) g.warps = g_gated_warps, g.split = 1;
   if (g_gated_split) g.split = g_gated_split;
   if (g.split > 1) g.warps = 8;

@@ -5,8 +5,8 @@ namespace mssm {
 
 template <typename T, int W, bool Z, bool CL>
 static cudaError_t scan_v(const GatedArgs& a, cudaStream_t s) {
-  if (a.cu) return gated_launch(gated_scan_kernel<T, kGs, W, Z, true, CL>, a, W, 0, s);
-  return gated_launch(gated_scan_kernel<T, kGs, W, Z, false, CL>, a, W, 0, s);
+  if (a.cu) return gated_launch(gated_scan_kernel<T, W, Z, true, CL>, a, W, 0, s);
+  return gated_launch(gated_scan_kernel<T, W, Z, false, CL>, a, W, 0, s);
 }
 
 template <typename T, int W, bool CL>
@@ -18,6 +18,7 @@ template <typename T>
 static cudaError_t scan_t(const GatedArgs& a, int warps, cudaStream_t s) {
   if (a.split > 1) return scan_w<T, 8, true>(a, s);
   return warps == 1 ? scan_w<T, 1, false>(a, s)
+         : warps == 2 ? scan_w<T, 2, false>(a, s)
          : warps == 4 ? scan_w<T, 4, false>(a, s) : scan_w<T, 8, false>(a, s);
 }
 

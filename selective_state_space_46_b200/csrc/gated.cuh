@@ -5,10 +5,10 @@
 //   out_t = h_t silu(z_t)                                               (z optional)
 //
 // One state per channel, so unlike the 16-state selective scan the path is a stream: 8 bytes of
-// bf16 I/O per element (10 with z) against five (six) SFU results.  A row's steps run along the
-// lanes: every thread holds kGs consecutive steps (one 16-byte vector of bf16), reduces them to
-// the affine map h -> A h + B, and the maps are composed by warp shuffles, across warps through
-// shared memory, and from tile to tile by a carry in registers.
+// bf16 I/O per element (10 with z) against three (four) SFU results and some 40 instructions.  A row's
+// steps run along the lanes: every thread holds kGs consecutive steps (one 16-byte vector of bf16), reduces
+// them to the affine map h -> A h + B, and the maps are composed by warp shuffles, across warps through
+// shared memory, and from tile to tile by a carry in registers; the next tile's loads are in flight meanwhile.
 #pragma once
 
 #include <cstdint>
@@ -89,38 +89,50 @@ __device__ __forceinline__ float logistic_exact(float v) {
 
 // per-channel constants of a row
 struct GatedRow {
-  float rate;    // c softplus(lam)
-  float root;    // sqrt(2 rate)
-  float cr, ci;  // -log2(e) times the biases
-  bool slow;     // some gate may take rate r past the series of the decay: CARE
+  float rate;          // c softplus(lam)
+  float cr, ci;        // -log2(e) times the biases
+  bool slow;           // some gate may take y = rate r to 1/8: CARE
+  // Polynomials of y on [0, 1/8] as polynomials of r, near-minimax fits with relative errors below 2^-25.
+  // (A decay of 0.9 to 0.999 at r = 1, the usual start, has a rate of 0.001 to 0.105.)
+  float a1, a2, a3, a4;  // exp(-y) = 1 + a1 r + ...: a fit of (1 - exp(-y)) / y
+  float p0, p1, p2, p3;  // sqrt(2 rate) P(y), P = sqrt((1 - exp(-2y)) / (2y))
 };
 
+constexpr float kFastEnd = 0.125f;
 constexpr float kSeriesEnd = 0.25f;
 
 template <typename Args>
 __device__ __forceinline__ GatedRow gated_row(const Args& p, int d) {
   GatedRow w;
-  w.rate = p.c * softplus_exact(p.lam[d * p.lam_s]);
-  w.root = sqrtf(2.0f * w.rate);
+  const float q = p.c * softplus_exact(p.lam[d * p.lam_s]), q2 = q * q;
+  w.rate = q;
   w.cr = p.rb ? -kLog2e * p.rb[d * p.rb_s] : 0.0f;
   w.ci = p.ib ? -kLog2e * p.ib[d * p.ib_s] : 0.0f;
-  w.slow = !(w.rate < kSeriesEnd);
+  w.slow = !(q < kFastEnd);
+  w.a1 = -q;
+  w.a2 = 0.499997109f * q2;
+  w.a3 = -0.166526049f * q2 * q;
+  w.a4 = 0.0397158563f * q2 * q2;
+  const float root = sqrtf(2.0f * q);
+  w.p0 = root;
+  w.p1 = -0.499995232f * root * q;
+  w.p2 = 0.208102137f * root * q2;
+  w.p3 = -0.0592916161f * root * q2 * q;
   return w;
 }
 
-// sigmoid(v) = 1 / p, p = 1 + 2^(-log2(e) v).
+// sigmoid(v) = 1 / p, p = 1 + e, e = 2^(-log2(e) v).
 //
 // The usual path (CARE = false) takes one reciprocal root for all gates of a step,
-//   u = 1 / (sqrt(pr) pi pz),  sqrt(r) = u pi pz,  sqrt(r) i = u pz,  1 / pz = (u pi)(pr sqrt(r)),
-// and none for sqrt(1 - a^2): with y = rate r, below y = 1/4,
-//   sqrt(1 - exp(-2y)) = sqrt(2 rate) sqrt(r) P(y),   P(y) = sqrt((1 - exp(-2y)) / (2y)),
-// a polynomial (its reciprocal R is another).  3 SFU results a step, 4 with z; a reciprocal each and two
-// roots would be 5 and 7, which is more than the I/O lets the SFU have (2.7 steps a cycle and SM of 10 bytes).
-// The polynomials are near-minimax fits on [0, 1/4], relative errors below 2^-27.
+//   u = 1 / (sqrt(pr) pi pz),  s = sqrt(r) = u pi pz,  sqrt(r) i = u pz,  1 / pz = (u pi)(pr s),
+// and none for sqrt(1 - a^2) = sqrt(2 rate) sqrt(r) P(y), y = rate r < 1/8.  3 SFU results a step, 4 with z, and
+// about 18 (25) packed instructions for two steps; what bounds the scan is the issue of instructions, so
+// the polynomials take r and have the row's rate in their coefficients, and products with 1 + e are
+// single fused instructions.
 //
-// `most` collects pr pi^2 pz^2, which has to stay below 2^125 for this; where it does not, or is a NaN, the
+// `most` adds up pr pi^2 pz^2, which has to stay below 2^125 for this; where it does not, or is a NaN, the
 // window is computed once more with CARE: a reciprocal for each gate, so every gate falls to the smallest
-// normal number before it is zero, and a NaN stays with its own gate.  Rows whose rate reaches 1/4 take
+// normal number before it is zero, and a NaN stays with its own gate.  Rows whose rate reaches 1/8 take
 // CARE at once.
 constexpr float kGateMost = 4.2535296e37f;  // 2^125
 
@@ -140,11 +152,7 @@ __device__ __forceinline__ f2_t rsqrt_2(f2_t v) {
   return f2(rsqrt_approx(a), rsqrt_approx(b));
 }
 __device__ __forceinline__ f2_t one_plus(f2_t v) { return add2(v, f2s(1.0f)); }
-__device__ __forceinline__ void note_most(float& most, f2_t v) {
-  float a, b;
-  f2split(v, a, b);
-  most = max_nan(most, max_nan(a, b));
-}
+__device__ __forceinline__ bool in_range(f2_t most) { return f2lo(most) + f2hi(most) < kGateMost; }
 
 // CARE: a sigmoid and its complement, which is 1 long before e / (1 + e) overflows
 __device__ __forceinline__ void sigmoid_both(f2_t v, f2_t& s, f2_t& c) {
@@ -154,26 +162,30 @@ __device__ __forceinline__ void sigmoid_both(f2_t v, f2_t& s, f2_t& c) {
   c = f2(f2lo(e) < 1.0e18f ? f2lo(q) : 1.0f, f2hi(e) < 1.0e18f ? f2hi(q) : 1.0f);
 }
 
-// 1 - exp(-y), y < 1/4.  With a = 1 minus it, a is rounded once: a relative error e of a slow decay compounds
-// over its memory to e / y, and the SFU exponential's 2^-22 would be felt.
-__device__ __forceinline__ f2_t decay_loss(f2_t y) {
+// exp(-y) for y < 1/8 by its polynomial, rounded once: a relative error e of a slow decay compounds over its
+// memory to e / y, and the SFU exponential's 2^-22 would be felt.
+__device__ __forceinline__ f2_t decay(f2_t r, const GatedRow& w) {
+  f2_t q = fma2(r, f2s(w.a4), f2s(w.a3));
+  q = fma2(r, q, f2s(w.a2));
+  q = fma2(r, q, f2s(w.a1));
+  return fma2(r, q, f2s(1.0f));
+}
+__device__ __forceinline__ f2_t root_series(f2_t r, const GatedRow& w) {  // sqrt(2 rate) P
+  f2_t q = fma2(r, f2s(w.p3), f2s(w.p2));
+  q = fma2(r, q, f2s(w.p1));
+  return fma2(r, q, f2s(w.p0));
+}
+// sqrt(rate / 2) / P(y); -y
+__device__ __forceinline__ f2_t root_inverse(f2_t ny, float half_root) {
+  f2_t q = fma2(ny, f2s(0.0211378392f), f2s(0.0416868366f));
+  q = fma2(ny, q, f2s(-0.499999613f));
+  return mul2(fma2(ny, q, f2s(1.0f)), f2s(half_root));
+}
+__device__ __forceinline__ f2_t decay_loss(f2_t y) {  // 1 - exp(-y), y < 1/4
   f2_t q = fma2(y, f2s(0.00753015606f), f2s(-0.0415001251f));
   q = fma2(y, q, f2s(0.166652888f));
   q = fma2(y, q, f2s(-0.499999642f));
-  q = fma2(y, q, f2s(1.0f));
-  return mul2(y, q);
-}
-__device__ __forceinline__ f2_t root_series(f2_t y) {  // P
-  f2_t q = fma2(y, f2s(0.0123667913f), f2s(-0.0622208975f));
-  q = fma2(y, q, f2s(0.208310276f));
-  q = fma2(y, q, f2s(-0.499999404f));
-  return fma2(y, q, f2s(1.0f));
-}
-__device__ __forceinline__ f2_t root_inverse(f2_t y) {  // R
-  f2_t q = fma2(y, f2s(-0.000555377337f), f2s(-0.0210434105f));
-  q = fma2(y, q, f2s(0.041683875f));
-  q = fma2(y, q, f2s(0.499999553f));
-  return fma2(y, q, f2s(1.0f));
+  return mul2(y, fma2(y, q, f2s(1.0f)));
 }
 
 // CARE: a, sqrt(1 - a^2) and y / sqrt(1 - a^2) for any y.  Above 1/4, 1 - a >= 0.22 and the SFU exponential
@@ -194,156 +206,134 @@ __device__ __forceinline__ void decay_care(f2_t y, f2_t& a, f2_t& beta, f2_t& y_
   y_beta = mul2(mul2(y, f2s(kVScale)), q);
 }
 
-// A window's a, driven terms b = sqrt(1 - a^2) i x and, with Z, silu(z) (in zz).  Returns `most`.
-template <bool Z, bool CARE, int E>
-__device__ __forceinline__ float steps(const f2_t (&x)[E / 2], const f2_t (&rr)[E / 2], const f2_t (&ii)[E / 2],
-                                       f2_t (&zz)[E / 2], const GatedRow& w, float (&av)[E], float (&bv)[E]) {
-  float most = 0.0f;
-#pragma unroll
-  for (int k = 0; k < E / 2; ++k) {
-    const f2_t pr = one_plus(ex2_2(fma2(rr[k], f2s(-kLog2e), f2s(w.cr))));
-    const f2_t pi = one_plus(ex2_2(fma2(ii[k], f2s(-kLog2e), f2s(w.ci))));
-    const f2_t pz = Z ? one_plus(ex2_2(mul2(zz[k], f2s(-kLog2e)))) : 0;
-    f2_t a, b;
-    if constexpr (CARE) {
-      f2_t beta, unused;
-      decay_care(mul2(rcp_2(pr), f2s(w.rate)), a, beta, unused);
-      b = mul2(mul2(beta, rcp_2(pi)), x[k]);
-      if (Z) zz[k] = mul2(zz[k], rcp_2(pz));
-    } else {
-      const f2_t t = Z ? mul2(pi, pz) : pi;
-      const f2_t all = mul2(mul2(pr, t), t);
-      note_most(most, all);
-      const f2_t u = rsqrt_2(all), s = mul2(u, t);
-      const f2_t y = mul2(mul2(s, s), f2s(w.rate));
-      a = fma2(decay_loss(y), f2s(-1.0f), f2s(1.0f));
-      b = mul2(mul2(mul2(Z ? mul2(u, pz) : u, f2s(w.root)), root_series(y)), x[k]);
-      if (Z) zz[k] = mul2(mul2(mul2(u, pi), mul2(pr, s)), zz[k]);
-    }
-    f2split(a, av[2 * k], av[2 * k + 1]);
-    f2split(b, bv[2 * k], bv[2 * k + 1]);
+// Two steps' a, driven terms b = sqrt(1 - a^2) i x and, with Z, silu(z).
+template <bool Z, bool CARE>
+__device__ __forceinline__ void step_pair(f2_t x, f2_t rr, f2_t ii, f2_t zz, const GatedRow& w, f2_t& a, f2_t& b, f2_t& g,
+                                          f2_t& most) {
+  const f2_t er = ex2_2(fma2(rr, f2s(-kLog2e), f2s(w.cr))), ei = ex2_2(fma2(ii, f2s(-kLog2e), f2s(w.ci)));
+  const f2_t ez = Z ? ex2_2(mul2(zz, f2s(-kLog2e))) : 0, pi = one_plus(ei);
+  if constexpr (CARE) {
+    f2_t beta, unused;
+    decay_care(mul2(rcp_2(one_plus(er)), f2s(w.rate)), a, beta, unused);
+    b = mul2(mul2(beta, rcp_2(pi)), x);
+    if (Z) g = mul2(zz, rcp_2(one_plus(ez)));
+  } else {
+    const f2_t t = Z ? fma2(pi, ez, pi) : pi, tt = mul2(t, t), all = fma2(tt, er, tt);
+    most = add2(most, all);
+    const f2_t u = rsqrt_2(all), s = mul2(u, t), r = mul2(s, s);
+    a = decay(r, w);
+    b = mul2(mul2(Z ? fma2(u, ez, u) : u, root_series(r, w)), x);
+    if (Z) g = mul2(mul2(fma2(u, ei, u), fma2(er, s, s)), zz);
   }
-  return most;
 }
 
-// zeros the steps of a window that `valid` leaves out
-template <int E>
-__device__ __forceinline__ void blank(f2_t (&v)[E / 2], unsigned valid) {
-#pragma unroll
-  for (int k = 0; k < E / 2; ++k)
-    v[k] = f2(valid >> (2 * k) & 1u ? f2lo(v[k]) : 0.0f, valid >> (2 * k + 1) & 1u ? f2hi(v[k]) : 0.0f);
-}
-
-// The same for the backward pass.  In: x, r, i, z, dout.  Out: y = rate r (x), 1 - r (r), i x rho (i),
-// dout silu'(z) (z), dout silu(z) (g), sqrt(1 - a^2) i (pv), b (1 - i) (cv), a and b.  `valid`: the steps
-// that count; y is 0 at the others.
-template <bool Z, bool CARE, int E>
-__device__ __forceinline__ float steps_grad(f2_t (&xv)[E / 2], f2_t (&rv)[E / 2], f2_t (&iv)[E / 2], f2_t (&zv)[E / 2],
-                                            f2_t (&gv)[E / 2], const GatedRow& w, bool whole, unsigned valid,
-                                            float (&av)[E], float (&bv)[E], f2_t (&pv)[E / 2], f2_t (&cv)[E / 2]) {
-  float most = 0.0f;
-#pragma unroll
-  for (int k = 0; k < E / 2; ++k) {
-    const f2_t ur = fma2(rv[k], f2s(-kLog2e), f2s(w.cr)), ui = fma2(iv[k], f2s(-kLog2e), f2s(w.ci));
-    const f2_t uz = Z ? mul2(zv[k], f2s(-kLog2e)) : 0;
-    f2_t y, ic, sz = 0, szc = 0, a;
-    auto only_valid = [&] {
-      if (whole) return;
-      f2_t one[1] = {y};
-      blank<2>(one, valid >> (2 * k));
-      y = one[0];
-    };
-    if constexpr (CARE) {
-      f2_t r, i, beta, y_beta;
-      sigmoid_both(ur, r, rv[k]);
-      sigmoid_both(ui, i, ic);
-      if (Z) sigmoid_both(uz, sz, szc);
-      y = mul2(r, f2s(w.rate));
-      only_valid();
-      decay_care(y, a, beta, y_beta);
-      pv[k] = mul2(beta, i);
-      iv[k] = mul2(mul2(i, xv[k]), mul2(a, y_beta));
-    } else {
-      const f2_t er = ex2_2(ur), ei = ex2_2(ui), ez = Z ? ex2_2(uz) : 0;
-      const f2_t pr = one_plus(er), pi = one_plus(ei), pz = Z ? one_plus(ez) : 0;
-      const f2_t t = Z ? mul2(pi, pz) : pi;
-      const f2_t all = mul2(mul2(pr, t), t);
-      note_most(most, all);
-      const f2_t u = rsqrt_2(all), s = mul2(u, t), r = mul2(s, s), sp = mul2(pr, s);  // sp = 1 / s
-      const f2_t si = Z ? mul2(u, pz) : u;                                             // sqrt(r) i
-      ic = mul2(ei, mul2(si, sp));
-      if (Z) {
-        sz = mul2(mul2(u, pi), sp);
-        szc = mul2(ez, sz);
-      }
-      rv[k] = mul2(er, r);
-      y = mul2(r, f2s(w.rate));
-      only_valid();
-      a = fma2(decay_loss(y), f2s(-1.0f), f2s(1.0f));
-      const f2_t g = mul2(si, f2s(w.root));
-      pv[k] = mul2(g, root_series(y));
-      iv[k] = mul2(mul2(mul2(g, f2s(0.5f)), xv[k]), mul2(a, root_inverse(y)));
-    }
-    const f2_t b = mul2(pv[k], xv[k]);
-    xv[k] = y;
-    cv[k] = mul2(b, ic);
+// The same for the backward pass.  In: x, r, i, z, dout.  Out: -y (x), 1 - r (r), i x rho (i), dout silu'(z)
+// (z), dout silu(z) (g), sqrt(1 - a^2) i (pv), b (1 - i) (cv), a and b.
+template <bool Z, bool CARE>
+__device__ __forceinline__ void step_pair_grad(f2_t& x, f2_t& rr, f2_t& ii, f2_t& zz, f2_t& gg, const GatedRow& w,
+                                               f2_t& a, f2_t& b, f2_t& pv, f2_t& cv, f2_t& most) {
+  const f2_t ur = fma2(rr, f2s(-kLog2e), f2s(w.cr)), ui = fma2(ii, f2s(-kLog2e), f2s(w.ci));
+  const f2_t uz = Z ? mul2(zz, f2s(-kLog2e)) : 0;
+  f2_t ic, sz = 0, szc = 0;
+  if constexpr (CARE) {
+    f2_t r, i, beta, y_beta;
+    sigmoid_both(ur, r, rr);
+    sigmoid_both(ui, i, ic);
+    if (Z) sigmoid_both(uz, sz, szc);
+    const f2_t y = mul2(r, f2s(w.rate));
+    decay_care(y, a, beta, y_beta);
+    pv = mul2(beta, i);
+    ii = mul2(mul2(i, x), mul2(a, y_beta));
+    b = mul2(pv, x);
+    x = mul2(y, f2s(-1.0f));
+  } else {
+    const f2_t er = ex2_2(ur), ei = ex2_2(ui), ez = Z ? ex2_2(uz) : 0, pi = one_plus(ei);
+    const f2_t t = Z ? fma2(pi, ez, pi) : pi, tt = mul2(t, t), all = fma2(tt, er, tt);
+    most = add2(most, all);
+    const f2_t u = rsqrt_2(all), s = mul2(u, t), sp = fma2(er, s, s);  // sp = 1 / s
+    const f2_t si = Z ? fma2(u, ez, u) : u;                            // sqrt(r) i
+    const f2_t r = mul2(s, s);
+    ic = mul2(ei, mul2(si, sp));
     if (Z) {
-      const f2_t ds = mul2(gv[k], sz);
-      gv[k] = mul2(ds, zv[k]);
-      zv[k] = mul2(ds, fma2(zv[k], szc, f2s(1.0f)));
+      sz = mul2(fma2(u, ei, u), sp);
+      szc = mul2(ez, sz);
     }
-    f2split(a, av[2 * k], av[2 * k + 1]);
-    f2split(b, bv[2 * k], bv[2 * k + 1]);
+    rr = mul2(er, r);
+    const f2_t ny = mul2(r, f2s(w.a1));
+    a = decay(r, w);
+    pv = mul2(si, root_series(r, w));
+    ii = mul2(mul2(si, x), mul2(a, root_inverse(ny, 0.5f * w.p0)));
+    b = mul2(pv, x);
+    x = ny;
   }
-  return most;
+  cv = mul2(b, ic);
+  if (Z) {
+    const f2_t ds = mul2(gg, sz);
+    gg = mul2(ds, zz);
+    zz = mul2(ds, fma2(zz, szc, f2s(1.0f)));
+  }
 }
 
 // ---------------------------------------------------------------- a thread's window of a row
 
-// E consecutive elements as stored
-template <typename T, int E>
+// A thread's kGs = 8 consecutive steps are 4 pairs of steps k and k + 4: two chains of 4 that the recurrence runs
+// through together and joins once.
+constexpr int kH = kGs / 2;
+
+__device__ __forceinline__ float of(const f2_t (&f)[kH], int e) { return e < kH ? f2lo(f[e]) : f2hi(f[e - kH]); }
+__device__ __forceinline__ void set(f2_t (&f)[kH], int e, float v) {
+  f[e % kH] = e < kH ? f2(v, f2hi(f[e])) : f2(f2lo(f[e - kH]), v);
+}
+// 1 for the steps of `mask` and 0 for the others
+__device__ __forceinline__ f2_t ones(unsigned mask, int k) {
+  return f2(mask >> k & 1u ? 1.0f : 0.0f, mask >> (k + kH) & 1u ? 1.0f : 0.0f);
+}
+// zeros the steps of a window that `valid` leaves out
+__device__ __forceinline__ void blank(f2_t (&v)[kH], unsigned valid) {
+#pragma unroll
+  for (int k = 0; k < kH; ++k)
+    v[k] = f2(valid >> k & 1u ? f2lo(v[k]) : 0.0f, valid >> (k + kH) & 1u ? f2hi(v[k]) : 0.0f);
+}
+
+// the steps as stored
+template <typename T>
 struct Win {
-  static constexpr int kVecs = E * int(sizeof(T)) / 16;
+  static constexpr int kVecs = kGs * int(sizeof(T)) / 16;
   uint4 v[kVecs];
 };
 
-// ... and as fp32 pairs
-template <typename T, int E>
-__device__ __forceinline__ void win_get(const Win<T, E>& w, f2_t (&f)[E / 2]) {
+template <typename T>
+__device__ __forceinline__ void win_get(const Win<T>& w, f2_t (&f)[kH]) {
   if constexpr (sizeof(T) == 2) {
-#pragma unroll
-    for (int k = 0; k < Win<T, E>::kVecs; ++k) {
-      f[4 * k] = f2(bf16lo(w.v[k].x), bf16hi(w.v[k].x));
-      f[4 * k + 1] = f2(bf16lo(w.v[k].y), bf16hi(w.v[k].y));
-      f[4 * k + 2] = f2(bf16lo(w.v[k].z), bf16hi(w.v[k].z));
-      f[4 * k + 3] = f2(bf16lo(w.v[k].w), bf16hi(w.v[k].w));
-    }
+    f[0] = f2(bf16lo(w.v[0].x), bf16lo(w.v[0].z));
+    f[1] = f2(bf16hi(w.v[0].x), bf16hi(w.v[0].z));
+    f[2] = f2(bf16lo(w.v[0].y), bf16lo(w.v[0].w));
+    f[3] = f2(bf16hi(w.v[0].y), bf16hi(w.v[0].w));
   } else {
-#pragma unroll
-    for (int k = 0; k < Win<T, E>::kVecs; ++k) {
-      f[2 * k] = f2(__uint_as_float(w.v[k].x), __uint_as_float(w.v[k].y));
-      f[2 * k + 1] = f2(__uint_as_float(w.v[k].z), __uint_as_float(w.v[k].w));
-    }
+    f[0] = f2(__uint_as_float(w.v[0].x), __uint_as_float(w.v[1].x));
+    f[1] = f2(__uint_as_float(w.v[0].y), __uint_as_float(w.v[1].y));
+    f[2] = f2(__uint_as_float(w.v[0].z), __uint_as_float(w.v[1].z));
+    f[3] = f2(__uint_as_float(w.v[0].w), __uint_as_float(w.v[1].w));
   }
 }
 
-// Steps [t0, t0 + E) of a row of L steps.  vec: the window's address is 16-byte aligned.  Steps
-// outside the row are not read and come back as zero.
-template <typename T, int E>
-__device__ __forceinline__ Win<T, E> win_load(const T* row, int t0, int L, bool vec) {
-  Win<T, E> w;
-  if (vec && t0 >= 0 && t0 + E <= L) {
-    const uint4* p = reinterpret_cast<const uint4*>(row + t0);
+// The thread's steps of the warp's window [wt, wt + 32 kGs) of a row of L steps.  inner: the window lies inside the
+// row and on a 16-byte boundary.  Steps outside the row are not read and come back as zero.
+template <typename T>
+__device__ __forceinline__ Win<T> win_load(const T* row, int wt, int lane, int L, bool inner) {
+  Win<T> w;
+  if (inner) {
+    const uint4* p = reinterpret_cast<const uint4*>(row + wt) + lane * Win<T>::kVecs;
 #pragma unroll
-    for (int k = 0; k < Win<T, E>::kVecs; ++k) w.v[k] = __ldg(p + k);
+    for (int k = 0; k < Win<T>::kVecs; ++k) w.v[k] = __ldg(p + k);
     return w;
   }
-  uint32_t u[4 * Win<T, E>::kVecs];
+  uint32_t u[4 * Win<T>::kVecs];
 #pragma unroll
-  for (int k = 0; k < 4 * Win<T, E>::kVecs; ++k) u[k] = 0u;
+  for (int k = 0; k < 4 * Win<T>::kVecs; ++k) u[k] = 0u;
 #pragma unroll
-  for (int j = 0; j < E; ++j) {
-    const int t = t0 + j;
+  for (int j = 0; j < kGs; ++j) {
+    const int t = wt + lane * kGs + j;
     if (t < 0 || t >= L) continue;
     if constexpr (sizeof(T) == 2) {
       u[j / 2] |= uint32_t(row[t]) << (16 * (j & 1));
@@ -352,36 +342,35 @@ __device__ __forceinline__ Win<T, E> win_load(const T* row, int t0, int L, bool 
     }
   }
 #pragma unroll
-  for (int k = 0; k < Win<T, E>::kVecs; ++k) w.v[k] = make_uint4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
+  for (int k = 0; k < Win<T>::kVecs; ++k) w.v[k] = make_uint4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
   return w;
 }
 
-// Stores the steps of `mask` (bit j: step t0 + j, which lies inside the row).
-template <typename T, int E>
-__device__ __forceinline__ void win_store(T* row, int t0, unsigned mask, bool vec, const f2_t (&f)[E / 2]) {
-  if (vec && mask == (1u << E) - 1u) {
-    uint4* p = reinterpret_cast<uint4*>(row + t0);
-#pragma unroll
-    for (int k = 0; k < Win<T, E>::kVecs; ++k) {
-      if constexpr (sizeof(T) == 2) {
-        p[k] = make_uint4(pack_bf16x2(f2lo(f[4 * k]), f2hi(f[4 * k])), pack_bf16x2(f2lo(f[4 * k + 1]), f2hi(f[4 * k + 1])),
-                          pack_bf16x2(f2lo(f[4 * k + 2]), f2hi(f[4 * k + 2])),
-                          pack_bf16x2(f2lo(f[4 * k + 3]), f2hi(f[4 * k + 3])));
-      } else {
-        p[k] = make_uint4(__float_as_uint(f2lo(f[2 * k])), __float_as_uint(f2hi(f[2 * k])),
-                          __float_as_uint(f2lo(f[2 * k + 1])), __float_as_uint(f2hi(f[2 * k + 1])));
-      }
+// Stores the steps of `mask` (bit j: the thread's step j, which lies inside the row).
+template <typename T>
+__device__ __forceinline__ void win_store(T* row, int wt, int lane, unsigned mask, bool inner, const f2_t (&f)[kH]) {
+  if (inner && mask == (1u << kGs) - 1u) {
+    uint4* p = reinterpret_cast<uint4*>(row + wt) + lane * Win<T>::kVecs;
+    if constexpr (sizeof(T) == 2) {
+      *p = make_uint4(pack_bf16x2(f2lo(f[0]), f2lo(f[1])), pack_bf16x2(f2lo(f[2]), f2lo(f[3])),
+                      pack_bf16x2(f2hi(f[0]), f2hi(f[1])), pack_bf16x2(f2hi(f[2]), f2hi(f[3])));
+    } else {
+      p[0] = make_uint4(__float_as_uint(f2lo(f[0])), __float_as_uint(f2lo(f[1])), __float_as_uint(f2lo(f[2])),
+                        __float_as_uint(f2lo(f[3])));
+      p[1] = make_uint4(__float_as_uint(f2hi(f[0])), __float_as_uint(f2hi(f[1])), __float_as_uint(f2hi(f[2])),
+                        __float_as_uint(f2hi(f[3])));
     }
     return;
   }
 #pragma unroll
-  for (int j = 0; j < E; ++j) {
+  for (int j = 0; j < kGs; ++j) {
     if (!(mask >> j & 1u)) continue;
-    const float v = j & 1 ? f2hi(f[j / 2]) : f2lo(f[j / 2]);
+    const float v = of(f, j);
+    T* to = row + wt + lane * kGs + j;
     if constexpr (sizeof(T) == 2) {
-      row[t0 + j] = f_to_bf16(v);
+      *to = f_to_bf16(v);
     } else {
-      row[t0 + j] = v;
+      *to = v;
     }
   }
 }
@@ -446,13 +435,12 @@ struct SeqWalk {
     const int before = base + __popc(below);
     return !__any_sync(~0u, v >= wt && v <= wt + n) && below != ~0u && before >= 1 && before <= S;
   }
-  template <int E>
   __device__ __forceinline__ SeqMask masks(int wt, int t0, int L, int lane) const {
     SeqMask m{0u, 0u, 0u, 0u, 0, false};
-    constexpr unsigned kAll = (1u << E) - 1u;
-    const int lo = max(max(c0, 0) - t0, 0), hi = min(min(cS, L) - t0, E);
-    if (hi > lo) m.valid = (kAll >> (E - hi)) & ~((1u << lo) - 1u);
-    const int te = wt + 32 * E;
+    constexpr unsigned kAll = (1u << kGs) - 1u;
+    const int lo = max(max(c0, 0) - t0, 0), hi = min(min(cS, L) - t0, kGs);
+    if (hi > lo) m.valid = (kAll >> (kGs - hi)) & ~((1u << lo) - 1u);
+    const int te = wt + 32 * kGs;
     m.below = base + __popc(__ballot_sync(~0u, v < wt));
     int o32 = v;
     for (int at = base;;) {
@@ -461,11 +449,11 @@ struct SeqWalk {
         const int o = __shfl_sync(~0u, o32, __ffs(in) - 1) - t0;
         in &= in - 1;
         if (o < 0) ++m.below;
-        if (o >= 0 && o < E) {
+        if (o >= 0 && o < kGs) {
           m.twice |= m.offs >> o & 1u;
           m.offs |= 1u << o;
         }
-        if (o >= 1 && o <= E) m.last |= 1u << (o - 1);
+        if (o >= 1 && o <= kGs) m.last |= 1u << (o - 1);
       }
       if (__any_sync(~0u, o32 > te)) break;
       at += 32;
@@ -607,32 +595,64 @@ __device__ __forceinline__ void check_offsets(const int* cu, int S, int L, unsig
   if (bad && err) atomicOr(err, 4u);
 }
 
-template <typename T, int E, bool Z>
-struct GatedIn {
-  Win<T, E> x, r, i, z;
-};
-
+// Warps of an SM for which registers are set aside: 80 registers a thread forward, 128 backward.  Measured
+// for 20 / 24 / 28 / 32 warps forward, 1x2048x131072 bf16: 535 / 522 / 563 / 557 us; for 12 / 16 / 20 backward,
+// 8x5120x4096 bf16: 901 / 819 / 901 us (fewer registers spill, fewer warps leave the issue slots idle).
+constexpr int kScanWarps = 24, kBwdWarps = 16;
 constexpr int gated_threads(int W) { return W == 1 ? 128 : 32 * W; }
 
 // the steps of a plain row's window that lie inside the row
-template <int E>
 __device__ __forceinline__ unsigned row_mask(int t0, int L) {
-  const int lo = max(-t0, 0), hi = min(L - t0, E);
-  return hi > lo ? ((1u << E) - 1u) >> (E - hi) & ~((1u << lo) - 1u) : 0u;
+  const int lo = max(-t0, 0), hi = min(L - t0, kGs);
+  return hi > lo ? ((1u << kGs) - 1u) >> (kGs - hi) & ~((1u << lo) - 1u) : 0u;
 }
 
-// W warps of a CTA share a row, with CL the CTAs of a cluster do; with W == 1 every warp has its own.
-template <typename T, int E, int W, bool Z, bool VL, bool CL>
-__global__ void __launch_bounds__(gated_threads(W)) gated_scan_kernel(const GatedArgs p) {
-  constexpr int kRows = W == 1 ? 4 : 1;
+// Where a CTA's warp works: W warps of a CTA share a row, with CL the CTAs of a cluster do; with W == 1 every
+// warp has its own.
+template <int W, bool CL>
+struct GatedPlace {
+  int warp, lane, split, rank;
+  int wc, wr;      // the warp's place among those of the row in the CTA, and among all
+  int64_t row;
+  __device__ __forceinline__ GatedPlace(const GatedArgs& p) {
+    warp = __shfl_sync(~0u, int(threadIdx.x) / 32, 0);
+    lane = threadIdx.x % 32;
+    split = CL ? p.split : 1;
+    rank = CL ? int(cluster_rank()) : 0;
+    wc = W == 1 ? 0 : warp;
+    wr = wc + rank * W;
+    row = CL ? blockIdx.x / split : W == 1 ? int64_t(blockIdx.x) * 4 + warp : int64_t(blockIdx.x);
+  }
+};
+
+// The map of a window whose steps all count: of its halves, and of all (A, B).
+struct WinMap {
+  float a_lo, b_lo, a_hi, b_hi;
+  float A, B;
+};
+__device__ __forceinline__ WinMap win_map(const f2_t (&a)[kH], const f2_t (&b)[kH]) {
+  f2_t aa = a[0], bb = b[0];
+#pragma unroll
+  for (int k = 1; k < kH; ++k) {
+    bb = fma2(a[k], bb, b[k]);
+    aa = mul2(aa, a[k]);
+  }
+  WinMap m;
+  f2split(aa, m.a_lo, m.a_hi);
+  f2split(bb, m.b_lo, m.b_hi);
+  m.A = m.a_lo * m.a_hi;
+  m.B = fmaf(m.a_hi, m.b_lo, m.b_hi);
+  return m;
+}
+
+template <typename T, int W, bool Z, bool VL, bool CL>
+__global__ void __launch_bounds__(gated_threads(W), kScanWarps * 32 / gated_threads(W)) gated_scan_kernel(const GatedArgs p) {
   __shared__ CarrySmem<W> sm;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (VL && blockIdx.x == 0) check_offsets(p.cu, p.S, p.L, p.err);
-  const int split = CL ? p.split : 1, rank = CL ? int(cluster_rank()) : 0;
-  const int64_t row = CL ? blockIdx.x / split : int64_t(blockIdx.x) * kRows + (W == 1 ? warp : 0);
-  if (row >= int64_t(p.Bt) * p.D) return;
-  const int bt = int(row / p.D), d = int(row % p.D);
-  const int wr = (W == 1 ? 0 : warp) + rank * W;  // the warp's place among those of the row
+  const GatedPlace<W, CL> at(p);
+  const int lane = at.lane;
+  if (at.row >= int64_t(p.Bt) * p.D) return;
+  const int bt = int(unsigned(at.row) / unsigned(p.D)), d = int(unsigned(at.row) % unsigned(p.D));  // Bt D < 2^31
   const T* x = static_cast<const T*>(p.x) + bt * p.x_sb + d * p.x_sd;
   const T* r = static_cast<const T*>(p.r) + bt * p.r_sb + d * p.r_sd;
   const T* i = static_cast<const T*>(p.i) + bt * p.i_sb + d * p.i_sd;
@@ -642,114 +662,117 @@ __global__ void __launch_bounds__(gated_threads(W)) gated_scan_kernel(const Gate
   const unsigned mis = misalign(x);
   const bool vec = misalign(r) == mis && misalign(i) == mis && misalign(out) == mis && (!Z || misalign(z) == mis);
   const int off = vec ? int(mis / sizeof(T)) : 0;
+  const int tile = 32 * W * kGs * at.split;
+  int wt = at.wr * 32 * kGs - off;
+  struct { Win<T> x, r, i, z; } nx;
+  auto fetch = [&](int t) {
+    const bool inner = vec && t >= 0 && t + 32 * kGs <= p.L;
+    nx.x = win_load<T>(x, t, lane, p.L, inner);
+    nx.r = win_load<T>(r, t, lane, p.L, inner);
+    nx.i = win_load<T>(i, t, lane, p.L, inner);
+    if (Z) nx.z = win_load<T>(z, t, lane, p.L, inner);
+  };
+  fetch(wt);
   float h = 0.0f;
   if (!VL && p.h0) h = p.h0[bt * p.h0_sb + d * p.h0_sd];
   SeqWalk walk;
   if (VL) {
     walk.start(p.cu, p.S, lane);
     if (p.last)
-      for (int j = wr * 32 + lane; j < p.S; j += 32 * W * split)
+      for (int j = at.wr * 32 + lane; j < p.S; j += 32 * W * at.split)
         if (p.cu[j] >= p.cu[j + 1])
           p.last[j * p.ls_sb + d * p.ls_sd] = p.h0 ? p.h0[j * p.h0_sb + d * p.h0_sd] : 0.0f;
   }
-  int flip = 0;
-  const int tile = 32 * W * E * split;
-  int wt = wr * 32 * E - off;
-  GatedIn<T, E, Z> nx;
-  auto fetch = [&](int t) {
-    nx.x = win_load<T, E>(x, t, p.L, vec);
-    nx.r = win_load<T, E>(r, t, p.L, vec);
-    nx.i = win_load<T, E>(i, t, p.L, vec);
-    if (Z) nx.z = win_load<T, E>(z, t, p.L, vec);
-  };
-  fetch(wt + lane * E);
   const GatedRow w = gated_row(p, d);
   if (CL) cluster_barrier();  // every CTA's shared memory is there
+  int flip = 0;
   for (int base = -off; base < p.L; base += tile, wt += tile) {
-    const int t0 = wt + lane * E;
-    f2_t xv[E / 2], rv[E / 2], iv[E / 2], zv[E / 2];
-    SeqMask m{(1u << E) - 1u, 0u, 0u, 0u, 0, false};
-    bool whole = wt >= 0 && wt + 32 * E <= p.L;
-    if (VL) whole = walk.enter(wt, 32 * E, lane) && whole;
+    const int t0 = wt + lane * kGs;
+    const bool inner = wt >= 0 && wt + 32 * kGs <= p.L;
+    SeqMask m{(1u << kGs) - 1u, 0u, 0u, 0u, 0, false};
+    bool whole = inner;
+    if (VL) whole = walk.enter(wt, 32 * kGs, lane) && whole;
     if (!whole) {
-      if (VL) m = walk.template masks<E>(wt, t0, p.L, lane);
-      else m.valid = row_mask<E>(t0, p.L);
+      if (VL) m = walk.masks(wt, t0, p.L, lane);
+      else m.valid = row_mask(t0, p.L);
     }
     float h0_first = 0.0f;  // of the window's first sequence start, asked for early
     if (VL && m.first && p.h0) h0_first = p.h0[int64_t(walk.seq(m, t0, __ffs(m.first) - 1)) * p.h0_sb + d * p.h0_sd];
+    f2_t xv[kH], rv[kH], iv[kH], zv[kH], a[kH], b[kH];
     auto unpack = [&] {
       win_get(nx.x, xv);
       win_get(nx.r, rv);
       win_get(nx.i, iv);
       if (Z) win_get(nx.z, zv);
       if (!whole) {  // steps outside count as zeros, whatever the tensors hold there
-        blank<E>(xv, m.valid);
-        blank<E>(rv, m.valid);
-        blank<E>(iv, m.valid);
-        if (Z) blank<E>(zv, m.valid);
+        blank(xv, m.valid);
+        blank(rv, m.valid);
+        blank(iv, m.valid);
+        if (Z) blank(zv, m.valid);
       }
     };
     unpack();
-    if (base + tile < p.L) fetch(t0 + tile);
-    float av[E], bv[E];
-    float A = 1.0f, B = 0.0f;
-    if (w.slow) {
-      steps<Z, true, E>(xv, rv, iv, zv, w, av, bv);
-    } else if (!(steps<Z, false, E>(xv, rv, iv, zv, w, av, bv) < kGateMost)) {
-      fetch(t0);
-      unpack();
-      if (base + tile < p.L) fetch(t0 + tile);
-      steps<Z, true, E>(xv, rv, iv, zv, w, av, bv);
-    }
-    if (whole) {
+    if (base + tile < p.L) fetch(wt + tile);
+    f2_t most = 0;
+    if (!w.slow) {
 #pragma unroll
-      for (int k = 0; k < E; ++k) {
-        B = fmaf(av[k], B, bv[k]);
-        A *= av[k];
+      for (int k = 0; k < kH; ++k) step_pair<Z, false>(xv[k], rv[k], iv[k], zv[k], w, a[k], b[k], zv[k], most);
+    }
+    if (w.slow || __any_sync(~0u, !in_range(most))) {
+      fetch(wt);
+      unpack();
+      if (base + tile < p.L) fetch(wt + tile);
+#pragma unroll
+      for (int k = 0; k < kH; ++k) step_pair<Z, true>(xv[k], rv[k], iv[k], zv[k], w, a[k], b[k], zv[k], most);
+    }
+    f2_t o[kH];
+    if (!VL || whole) {
+      if (!VL && !whole) {
+#pragma unroll
+        for (int k = 0; k < kH; ++k) {  // the identity outside the row
+          const f2_t on = ones(m.valid, k);
+          b[k] = mul2(b[k], on);
+          a[k] = fma2(a[k], on, fma2(on, f2s(-1.0f), f2s(1.0f)));
+        }
+      }
+      const WinMap wm = win_map(a, b);
+      const float in = tile_carry<VL, false, W, CL>(wm.A, wm.B, h, sm, flip, at.wc, lane, at.rank, at.split);
+      f2_t hh = f2(in, fmaf(wm.a_lo, in, wm.b_lo));
+#pragma unroll
+      for (int k = 0; k < kH; ++k) {
+        hh = fma2(a[k], hh, b[k]);
+        o[k] = Z ? mul2(hh, zv[k]) : hh;
       }
     } else {
+      float A = 1.0f, B = 0.0f;
 #pragma unroll
-      for (int k = 0; k < E; ++k) {
-        if (!(m.valid >> k & 1u)) av[k] = 1.0f, bv[k] = 0.0f;
-        if (VL && (m.first >> k & 1u)) {
+      for (int e = 0; e < kGs; ++e) {
+        float ca = of(a, e), cb = of(b, e);
+        if (!(m.valid >> e & 1u)) ca = 1.0f, cb = 0.0f;
+        if (m.first >> e & 1u) {
           if (p.h0) {
-            const bool early = (m.first & ((1u << k) - 1u)) == 0u;
-            bv[k] = fmaf(av[k], early ? h0_first : p.h0[int64_t(walk.seq(m, t0, k)) * p.h0_sb + d * p.h0_sd], bv[k]);
+            const bool early = (m.first & ((1u << e) - 1u)) == 0u;
+            cb = fmaf(ca, early ? h0_first : p.h0[int64_t(walk.seq(m, t0, e)) * p.h0_sb + d * p.h0_sd], cb);
           }
-          av[k] = kResetA;
+          ca = kResetA;
         }
-        float ca = av[k], cb = bv[k];
+        set(a, e, ca);
+        set(b, e, cb);
         compose<VL>(ca, cb, A, B);
         A = ca;
         B = cb;
       }
-    }
-    float hk = tile_carry<VL, false, W, CL>(A, B, h, sm, flip, W == 1 ? 0 : warp, lane, rank, split);
-    f2_t ov[E / 2];
-    if (!VL || whole) {
+      float hk = tile_carry<VL, false, W, CL>(A, B, h, sm, flip, at.wc, lane, at.rank, at.split);
 #pragma unroll
-      for (int k = 0; k < E / 2; ++k) {
-        const float h0 = fmaf(av[2 * k], hk, bv[2 * k]);
-        hk = fmaf(av[2 * k + 1], h0, bv[2 * k + 1]);
-        ov[k] = Z ? mul2(f2(h0, hk), zv[k]) : f2(h0, hk);
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < E / 2; ++k) {
-        float o[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int e = 2 * k + q;
-          hk = apply<VL>(av[e], bv[e], hk);
-          if ((m.last >> e & 1u) && p.last) p.last[int64_t(walk.seq(m, t0, e)) * p.ls_sb + d * p.ls_sd] = hk;
-          o[q] = hk;
-        }
-        ov[k] = Z ? mul2(f2(o[0], o[1]), zv[k]) : f2(o[0], o[1]);
+      for (int e = 0; e < kGs; ++e) {
+        hk = apply<VL>(of(a, e), of(b, e), hk);
+        if ((m.last >> e & 1u) && p.last) p.last[int64_t(walk.seq(m, t0, e)) * p.ls_sb + d * p.ls_sd] = hk;
+        set(o, e, Z ? hk * of(zv, e) : hk);
       }
     }
-    win_store<T, E>(out, t0, m.valid, vec, ov);
+    win_store(out, wt, lane, m.valid, vec && inner, o);
   }
-  if (!VL && p.last && lane == 0 && wr == 0) p.last[bt * p.ls_sb + d * p.ls_sd] = h;
+  if (!VL && p.last && lane == 0 && at.wr == 0) p.last[bt * p.ls_sb + d * p.ls_sd] = h;
 }
 
 // ---------------------------------------------------------------- backward
@@ -764,20 +787,18 @@ __global__ void __launch_bounds__(gated_threads(W)) gated_scan_kernel(const Gate
 // The row is swept forward once, keeping the state before every tile, then backwards tile by tile,
 // recomputing the states inside the tile: the second read finds the row in L2.  A row of one tile is
 // read once.
-template <typename T, int E, int W, bool Z, bool VL, bool CL>
-__global__ void __launch_bounds__(gated_threads(W)) gated_bwd_kernel(const GatedArgs p) {
-  constexpr int kRows = W == 1 ? 4 : 1;
+template <typename T, int W, bool Z, bool VL, bool CL>
+__global__ void __launch_bounds__(gated_threads(W), kBwdWarps * 32 / gated_threads(W)) gated_bwd_kernel(const GatedArgs p) {
   __shared__ CarrySmem<W> sm;
   __shared__ float s_red[3][W];
   __shared__ float s_sum[3][kMaxSplit];
-  extern __shared__ float s_ckpt[];  // [kRows][ntiles]
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  extern __shared__ float s_ckpt[];  // [rows of the CTA][ntiles]
   if (VL && blockIdx.x == 0) check_offsets(p.cu, p.S, p.L, p.err);
-  const int split = CL ? p.split : 1, rank = CL ? int(cluster_rank()) : 0;
-  const int64_t row = CL ? blockIdx.x / split : int64_t(blockIdx.x) * kRows + (W == 1 ? warp : 0);
+  const GatedPlace<W, CL> at(p);
+  const int lane = at.lane, warp = at.warp, wc = at.wc, wr = at.wr, split = at.split, rank = at.rank;
+  const int64_t row = at.row;
   if (row >= int64_t(p.Bt) * p.D) return;
-  const int bt = int(row / p.D), d = int(row % p.D);
-  const int wc = W == 1 ? 0 : warp, wr = wc + rank * W;
+  const int bt = int(unsigned(row) / unsigned(p.D)), d = int(unsigned(row) % unsigned(p.D));  // Bt D < 2^31
   float* ckpt = s_ckpt + (W == 1 ? warp * p.ntiles : 0);
   const T* x = static_cast<const T*>(p.x) + bt * p.x_sb + d * p.x_sd;
   const T* r = static_cast<const T*>(p.r) + bt * p.r_sb + d * p.r_sd;
@@ -792,6 +813,26 @@ __global__ void __launch_bounds__(gated_threads(W)) gated_bwd_kernel(const Gated
   const bool vec = misalign(r) == mis && misalign(i) == mis && misalign(gy) == mis && misalign(dx) == mis &&
                    misalign(dr) == mis && misalign(di) == mis && (!Z || (misalign(z) == mis && misalign(dz) == mis));
   const int off = vec ? int(mis / sizeof(T)) : 0;
+  const int tile = 32 * W * kGs * split;
+  const int ntiles = (p.L + off + tile - 1) / tile;
+  const int lane0 = wr * 32 * kGs - off;  // the warp's first step in the first tile
+  struct { Win<T> x, r, i; } nx;
+  Win<T> nz, ng;
+  auto inner_at = [&](int t) { return t >= 0 && t + 32 * kGs <= p.L; };
+  auto fetch = [&](int t) {
+    const bool inner = vec && inner_at(t);
+    nx.x = win_load<T>(x, t, lane, p.L, inner);
+    nx.r = win_load<T>(r, t, lane, p.L, inner);
+    nx.i = win_load<T>(i, t, lane, p.L, inner);
+  };
+  auto fetch_all = [&](int t) {
+    const bool inner = vec && inner_at(t);
+    fetch(t);
+    ng = win_load<T>(gy, t, lane, p.L, inner);
+    if (Z) nz = win_load<T>(z, t, lane, p.L, inner);
+  };
+  if (ntiles > 1) fetch(lane0);
+  else if (ntiles > 0) fetch_all(lane0);
   SeqWalk walk;
   if (VL) {
     walk.start(p.cu, p.S, lane);
@@ -800,253 +841,227 @@ __global__ void __launch_bounds__(gated_threads(W)) gated_bwd_kernel(const Gated
         if (p.cu[j] >= p.cu[j + 1])
           p.dh0[j * p.dh_sb + d * p.dh_sd] = p.dlast ? p.dlast[j * p.dl_sb + d * p.dl_sd] : 0.0f;
   }
-  const int tile = 32 * W * E * split;
-  const int ntiles = (p.L + off + tile - 1) / tile;
-  const int lane0 = wr * 32 * E - off;  // the warp's first step in the first tile
+  const GatedRow w = gated_row(p, d);
+  if (CL) cluster_barrier();  // every CTA's shared memory is there
   int flip = 0;
+  SeqMask m;
+  bool whole;
+  float h0_first;  // of the window's first sequence start, asked for early
+  auto enter = [&](int wt) {
+    m = SeqMask{(1u << kGs) - 1u, 0u, 0u, 0u, 0, false};
+    whole = inner_at(wt);
+    if (VL) whole = walk.enter(wt, 32 * kGs, lane) && whole;
+    if (!whole) {
+      if (VL) m = walk.masks(wt, wt + lane * kGs, p.L, lane);
+      else m.valid = row_mask(wt + lane * kGs, p.L);
+    }
+    h0_first = 0.0f;
+    if (VL && m.first && p.h0)
+      h0_first = p.h0[int64_t(walk.seq(m, wt + lane * kGs, __ffs(m.first) - 1)) * p.h0_sb + d * p.h0_sd];
+  };
+  auto h0_at = [&](int t0, int e) {
+    if (!p.h0) return 0.0f;
+    const bool early = (m.first & ((1u << e) - 1u)) == 0u;
+    return early ? h0_first : p.h0[int64_t(walk.seq(m, t0, e)) * p.h0_sb + d * p.h0_sd];
+  };
+  f2_t xv[kH], rv[kH], iv[kH], zv[kH], gv[kH], a[kH], b[kH];
+  // steps outside count as zeros, whatever the tensors hold there
+  auto unpack = [&] {
+    win_get(nx.x, xv);
+    win_get(nx.r, rv);
+    win_get(nx.i, iv);
+    if (!whole) {
+      blank(xv, m.valid);
+      blank(rv, m.valid);
+      blank(iv, m.valid);
+    }
+  };
+  auto unpack_all = [&] {
+    unpack();
+    win_get(ng, gv);
+    if (Z) win_get(nz, zv);
+    if (!whole) {
+      blank(gv, m.valid);
+      if (Z) blank(zv, m.valid);
+    }
+  };
 
-  GatedRow w;
   // forward sweep: the state before every tile
   float h = !VL && p.h0 ? p.h0[bt * p.h0_sb + d * p.h0_sd] : 0.0f;
-  {
-    GatedIn<T, E, false> nx;
-    auto fetch = [&](int t) {
-      nx.x = win_load<T, E>(x, t, p.L, vec);
-      nx.r = win_load<T, E>(r, t, p.L, vec);
-      nx.i = win_load<T, E>(i, t, p.L, vec);
-    };
-    if (ntiles > 1) fetch(lane0 + lane * E);
-    w = gated_row(p, d);
-    if (CL) cluster_barrier();  // every CTA's shared memory is there
-    for (int tl = 0; tl + 1 < ntiles; ++tl) {
-      if (lane == 0 && wc == 0) ckpt[tl] = h;
-      const int wt = lane0 + tl * tile, t0 = wt + lane * E;
-      f2_t xv[E / 2], rv[E / 2], iv[E / 2];
-      SeqMask m{(1u << E) - 1u, 0u, 0u, 0u, 0, false};
-      bool whole = wt >= 0;  // only the last tile reaches the row's end
-      if (VL) whole = walk.enter(wt, 32 * E, lane) && whole;
-      if (!whole) {
-        if (VL) m = walk.template masks<E>(wt, t0, p.L, lane);
-        else m.valid = row_mask<E>(t0, p.L);
-      }
-      float h0_first = 0.0f;
-      if (VL && m.first && p.h0) h0_first = p.h0[int64_t(walk.seq(m, t0, __ffs(m.first) - 1)) * p.h0_sb + d * p.h0_sd];
-      auto unpack = [&] {
-        win_get(nx.x, xv);
-        win_get(nx.r, rv);
-        win_get(nx.i, iv);
-        if (!whole) {
-          blank<E>(xv, m.valid);
-          blank<E>(rv, m.valid);
-          blank<E>(iv, m.valid);
-        }
-      };
-      unpack();
-      if (tl + 2 < ntiles) fetch(t0 + tile);
-      float av[E], bv[E];
-      float A = 1.0f, B = 0.0f;
-      f2_t none[E / 2];
-      if (w.slow) {
-        steps<false, true, E>(xv, rv, iv, none, w, av, bv);
-      } else if (!(steps<false, false, E>(xv, rv, iv, none, w, av, bv) < kGateMost)) {
-        fetch(t0);
-        unpack();
-        if (tl + 2 < ntiles) fetch(t0 + tile);
-        steps<false, true, E>(xv, rv, iv, none, w, av, bv);
-      }
-      if (whole) {
-#pragma unroll
-        for (int k = 0; k < E; ++k) {
-          B = fmaf(av[k], B, bv[k]);
-          A *= av[k];
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < E; ++k) {
-          if (!(m.valid >> k & 1u)) av[k] = 1.0f, bv[k] = 0.0f;
-          if (VL && (m.first >> k & 1u)) {
-            if (p.h0) {
-            const bool early = (m.first & ((1u << k) - 1u)) == 0u;
-            bv[k] = fmaf(av[k], early ? h0_first : p.h0[int64_t(walk.seq(m, t0, k)) * p.h0_sb + d * p.h0_sd], bv[k]);
-          }
-            av[k] = kResetA;
-          }
-          float ca = av[k], cb = bv[k];
-          compose<VL>(ca, cb, A, B);
-          A = ca;
-          B = cb;
-        }
-      }
-      tile_carry<VL, false, W, CL>(A, B, h, sm, flip, wc, lane, rank, split);
-    }
-    if (lane == 0 && wc == 0 && ntiles > 0) ckpt[ntiles - 1] = h;
-  }
-  if (W == 1) __syncwarp();
-  else __syncthreads();
-
-  // backward sweep
-  float sum_w = 0.0f, sum_r = 0.0f, sum_i = 0.0f;
-  float c = !VL && p.dlast ? p.dlast[bt * p.dl_sb + d * p.dl_sd] : 0.0f;
-  GatedIn<T, E, Z> nx;
-  Win<T, E> ng;
-  auto fetch = [&](int t) {
-    nx.x = win_load<T, E>(x, t, p.L, vec);
-    nx.r = win_load<T, E>(r, t, p.L, vec);
-    nx.i = win_load<T, E>(i, t, p.L, vec);
-    ng = win_load<T, E>(gy, t, p.L, vec);
-    if (Z) nx.z = win_load<T, E>(z, t, p.L, vec);
-  };
-  if (ntiles > 0) fetch(lane0 + (ntiles - 1) * tile + lane * E);
-  for (int tl = ntiles - 1; tl >= 0; --tl) {
-    const int wt = lane0 + tl * tile, t0 = wt + lane * E;
-    f2_t xv[E / 2], rv[E / 2], iv[E / 2], zv[E / 2], gv[E / 2];
-    SeqMask m{(1u << E) - 1u, 0u, 0u, 0u, 0, false};
-    bool whole = wt >= 0 && wt + 32 * E <= p.L;
-    if (VL) whole = walk.enter(wt, 32 * E, lane) && whole;
-    if (!whole) {
-      if (VL) m = walk.template masks<E>(wt, t0, p.L, lane);
-      else m.valid = row_mask<E>(t0, p.L);
-    }
-    float h0_first = 0.0f;  // of the window's first sequence start, asked for early
-    if (VL && m.first && p.h0) h0_first = p.h0[int64_t(walk.seq(m, t0, __ffs(m.first) - 1)) * p.h0_sb + d * p.h0_sd];
-    auto unpack = [&] {
-      win_get(nx.x, xv);
-      win_get(nx.r, rv);
-      win_get(nx.i, iv);
-      win_get(ng, gv);
-      if (Z) win_get(nx.z, zv);
-      if (!whole) {  // steps outside count as zeros, whatever the tensors hold there
-        blank<E>(xv, m.valid);
-        blank<E>(rv, m.valid);
-        blank<E>(iv, m.valid);
-        blank<E>(gv, m.valid);
-        if (Z) blank<E>(zv, m.valid);
-      }
-    };
-    float dl_last = 0.0f;  // of the window's last sequence end
-    if (VL && m.last && p.dlast) dl_last = p.dlast[int64_t(walk.seq(m, t0, 31 - __clz(m.last))) * p.dl_sb + d * p.dl_sd];
+  for (int tl = 0; tl + 1 < ntiles; ++tl) {
+    if (lane == 0 && wc == 0) ckpt[tl] = h;
+    const int wt = lane0 + tl * tile, t0 = wt + lane * kGs;
+    enter(wt);
     unpack();
-    if (tl > 0) fetch(t0 - tile);
-    float av[E], bv[E];
-    f2_t pv[E / 2], cv[E / 2];
-    float A = 1.0f, B = 0.0f;
-    if (w.slow) {
-      steps_grad<Z, true, E>(xv, rv, iv, zv, gv, w, whole, m.valid, av, bv, pv, cv);
-    } else if (!(steps_grad<Z, false, E>(xv, rv, iv, zv, gv, w, whole, m.valid, av, bv, pv, cv) < kGateMost)) {
-      fetch(t0);
-      unpack();
-      if (tl > 0) fetch(t0 - tile);
-        steps_grad<Z, true, E>(xv, rv, iv, zv, gv, w, whole, m.valid, av, bv, pv, cv);
+    if (tl + 2 < ntiles) fetch(wt + tile);
+    else fetch_all(wt + tile);
+    f2_t most = 0, none;
+    if (!w.slow) {
+#pragma unroll
+      for (int k = 0; k < kH; ++k) step_pair<false, false>(xv[k], rv[k], iv[k], 0, w, a[k], b[k], none, most);
     }
-    float hk;
-    if (!VL || whole) {
+    if (w.slow || __any_sync(~0u, !in_range(most))) {
+      fetch(wt);
+      unpack();
+      if (tl + 2 < ntiles) fetch(wt + tile);
+      else fetch_all(wt + tile);
 #pragma unroll
-      for (int k = 0; k < E; ++k) {
-        B = fmaf(av[k], B, bv[k]);
-        A *= av[k];
-      }
-      float hin = ckpt[tl];
-      hk = tile_carry<VL, false, W, CL>(A, B, hin, sm, flip, wc, lane, rank, split);
-      // w / s = a (i x rho - y h_before), the outputs' gradients, and the adjoint's map of the window
-#pragma unroll
-      for (int k = 0; k < E / 2; ++k) {
-        const float h0 = fmaf(av[2 * k], hk, bv[2 * k]), h1 = fmaf(av[2 * k + 1], h0, bv[2 * k + 1]);
-        const f2_t y = xv[k];
-        xv[k] = mul2(f2(av[2 * k], av[2 * k + 1]), fma2(mul2(y, f2s(-1.0f)), f2(hk, h0), iv[k]));
-        if (Z) zv[k] = mul2(zv[k], f2(h0, h1));
-        hk = h1;
-      }
-      A = 1.0f;
-      B = 0.0f;
-#pragma unroll
-      for (int k = E - 1; k >= 0; --k) {
-        const float g = k & 1 ? f2hi(gv[k / 2]) : f2lo(gv[k / 2]);
-        B = av[k] * (g + B);
-        A *= av[k];
-      }
+      for (int k = 0; k < kH; ++k) step_pair<false, true>(xv[k], rv[k], iv[k], 0, w, a[k], b[k], none, most);
+    }
+    float A = 1.0f, B = 0.0f;
+    if (whole) {
+      const WinMap wm = win_map(a, b);
+      A = wm.A;
+      B = wm.B;
     } else {
-      float hb[E];
 #pragma unroll
-      for (int k = 0; k < E; ++k) {
-        hb[k] = 0.0f;
-        float ca = av[k], cb = bv[k];
-        if (m.first >> k & 1u) {
-          if (p.h0) {
-            const bool early = (m.first & ((1u << k) - 1u)) == 0u;
-            hb[k] = early ? h0_first : p.h0[int64_t(walk.seq(m, t0, k)) * p.h0_sb + d * p.h0_sd];
-          }
-          cb = fmaf(ca, hb[k], cb);
+      for (int e = 0; e < kGs; ++e) {
+        float ca = of(a, e), cb = of(b, e);
+        if (!(m.valid >> e & 1u)) ca = 1.0f, cb = 0.0f;
+        if (VL && (m.first >> e & 1u)) {
+          cb = fmaf(ca, h0_at(t0, e), cb);
           ca = kResetA;
         }
         compose<VL>(ca, cb, A, B);
         A = ca;
         B = cb;
       }
-      float hin = ckpt[tl];
-      hk = tile_carry<VL, false, W, CL>(A, B, hin, sm, flip, wc, lane, rank, split);
+    }
+    tile_carry<VL, false, W, CL>(A, B, h, sm, flip, wc, lane, rank, split);
+  }
+  if (lane == 0 && wc == 0 && ntiles > 0) ckpt[ntiles - 1] = h;
+  if (W == 1) __syncwarp();
+  else __syncthreads();
+
+  // backward sweep
+  f2_t acc_w = 0, acc_r = 0, acc_i = 0;
+  float c = !VL && p.dlast ? p.dlast[bt * p.dl_sb + d * p.dl_sd] : 0.0f;
+  for (int tl = ntiles - 1; tl >= 0; --tl) {
+    const int wt = lane0 + tl * tile, t0 = wt + lane * kGs;
+    const bool inner = vec && inner_at(wt);
+    enter(wt);
+    float dl_last = 0.0f;  // of the window's last sequence end
+    if (VL && m.last && p.dlast) dl_last = p.dlast[int64_t(walk.seq(m, t0, 31 - __clz(m.last))) * p.dl_sb + d * p.dl_sd];
+    unpack_all();
+    if (tl > 0) fetch_all(wt - tile);
+    f2_t pv[kH], cv[kH], most = 0;
+    if (!w.slow) {
 #pragma unroll
-      for (int k = 0; k < E; ++k) {
-        if (!(m.first >> k & 1u)) hb[k] = hk;
-        hk = fmaf(av[k], hb[k], bv[k]);
-        if (!(m.valid >> k & 1u)) hk = hb[k] = 0.0f;  // outside every sequence
-        bv[k] = hk;
+      for (int k = 0; k < kH; ++k)
+        step_pair_grad<Z, false>(xv[k], rv[k], iv[k], zv[k], gv[k], w, a[k], b[k], pv[k], cv[k], most);
+    }
+    if (w.slow || __any_sync(~0u, !in_range(most))) {
+      fetch_all(wt);
+      unpack_all();
+      if (tl > 0) fetch_all(wt - tile);
+#pragma unroll
+      for (int k = 0; k < kH; ++k)
+        step_pair_grad<Z, true>(xv[k], rv[k], iv[k], zv[k], gv[k], w, a[k], b[k], pv[k], cv[k], most);
+    }
+    if (!whole) {
+#pragma unroll
+      for (int k = 0; k < kH; ++k) {  // the identity outside: y = 0, a = 1 (b is 0 with x)
+        const f2_t on = ones(m.valid, k);
+        xv[k] = mul2(xv[k], on);
+        a[k] = fma2(a[k], on, fma2(on, f2s(-1.0f), f2s(1.0f)));
       }
+    }
+    // now xv: -y, rv: 1 - r, iv: i x rho, zv: dout silu'(z), gv: dout silu(z)
+    f2_t s[kH];
+    float hin = ckpt[tl];
+    if (!VL || whole) {
+      const WinMap wm = win_map(a, b);
+      const float in = tile_carry<VL, false, W, CL>(wm.A, wm.B, hin, sm, flip, wc, lane, rank, split);
+      // w / s = a (i x rho - y h_before), dz, and what flows back out of the halves
+      f2_t hh = f2(in, fmaf(wm.a_lo, in, wm.b_lo));
 #pragma unroll
-      for (int k = 0; k < E / 2; ++k) {
-        xv[k] = mul2(f2(av[2 * k], av[2 * k + 1]), fma2(mul2(xv[k], f2s(-1.0f)), f2(hb[2 * k], hb[2 * k + 1]), iv[k]));
-        if (Z) zv[k] = mul2(zv[k], f2(bv[2 * k], bv[2 * k + 1]));
+      for (int k = 0; k < kH; ++k) {
+        xv[k] = mul2(a[k], fma2(xv[k], hh, iv[k]));
+        hh = fma2(a[k], hh, b[k]);
+        if (Z) zv[k] = mul2(zv[k], hh);
       }
-      A = 1.0f;
-      B = 0.0f;
+      f2_t back = mul2(a[kH - 1], gv[kH - 1]);
 #pragma unroll
-      for (int k = E - 1; k >= 0; --k) {
-        float g = k & 1 ? f2hi(gv[k / 2]) : f2lo(gv[k / 2]);
-        const bool end = m.last >> k & 1u;
-        if (end && p.dlast) {
-          const bool early = (m.last >> k) == 1u;
-          g += early ? dl_last : p.dlast[int64_t(walk.seq(m, t0, k)) * p.dl_sb + d * p.dl_sd];
-          gv[k / 2] = k & 1 ? f2(f2lo(gv[k / 2]), g) : f2(g, f2hi(gv[k / 2]));
+      for (int k = kH - 2; k >= 0; --k) back = mul2(a[k], add2(gv[k], back));
+      float c_lo, c_hi;
+      f2split(back, c_lo, c_hi);
+      if (Z) win_store(dz, wt, lane, m.valid, inner, zv);
+      const float cin = tile_carry<VL, true, W, CL>(wm.A, fmaf(wm.a_lo, c_hi, c_lo), c, sm, flip, wc, lane, rank, split);
+      f2_t cc = f2(fmaf(wm.a_hi, cin, c_hi), cin);
+#pragma unroll
+      for (int k = kH - 1; k >= 0; --k) {
+        s[k] = add2(gv[k], cc);
+        cc = mul2(a[k], s[k]);
+      }
+    } else {
+      float hb[kGs], A = 1.0f, B = 0.0f;
+#pragma unroll
+      for (int e = 0; e < kGs; ++e) {
+        hb[e] = 0.0f;
+        float ca = of(a, e), cb = of(b, e);
+        if (m.first >> e & 1u) {
+          hb[e] = h0_at(t0, e);
+          cb = fmaf(ca, hb[e], cb);
+          ca = kResetA;
         }
-        float ca = end ? kResetA : av[k], cb = av[k] * g;
         compose<VL>(ca, cb, A, B);
         A = ca;
         B = cb;
       }
-    }
-    float ck = tile_carry<VL, true, W, CL>(A, B, c, sm, flip, wc, lane, rank, split);
-    float sv[E];
+      float hk = tile_carry<VL, false, W, CL>(A, B, hin, sm, flip, wc, lane, rank, split);
 #pragma unroll
-    for (int k = E - 1; k >= 0; --k) {
-      const float g = k & 1 ? f2hi(gv[k / 2]) : f2lo(gv[k / 2]);
-      sv[k] = VL && (m.last >> k & 1u) ? g : g + ck;
-      ck = av[k] * sv[k];
-      if (VL && (m.first >> k & 1u) && p.dh0)
-        p.dh0[int64_t(walk.seq(m, t0, k)) * p.dh_sb + d * p.dh_sd] = ck;
-      if (VL && !whole && !(m.valid >> k & 1u)) sv[k] = 0.0f;  // what flows past the steps outside stays out of the sums
-    }
-    f2_t acc_w = 0, acc_r = 0, acc_i = 0;
+      for (int e = 0; e < kGs; ++e) {
+        if (!(m.first >> e & 1u)) hb[e] = hk;
+        hk = fmaf(of(a, e), hb[e], of(b, e));
+        if (!(m.valid >> e & 1u)) hk = hb[e] = 0.0f;  // outside every sequence
+        set(b, e, hk);
+      }
 #pragma unroll
-    for (int k = 0; k < E / 2; ++k) {
-      const f2_t s = f2(sv[2 * k], sv[2 * k + 1]);
-      const f2_t ww = mul2(s, xv[k]);
-      const f2_t gr = mul2(rv[k], ww);
-      const f2_t gx = mul2(s, pv[k]);
-      const f2_t gi = mul2(s, cv[k]);
+      for (int k = 0; k < kH; ++k) {
+        xv[k] = mul2(a[k], fma2(xv[k], f2(hb[k], hb[k + kH]), iv[k]));
+        if (Z) zv[k] = mul2(zv[k], b[k]);
+      }
+      A = 1.0f;
+      B = 0.0f;
+#pragma unroll
+      for (int e = kGs - 1; e >= 0; --e) {
+        float g = of(gv, e);
+        const bool end = m.last >> e & 1u;
+        if (end && p.dlast) {
+          const bool early = (m.last >> e) == 1u;
+          g += early ? dl_last : p.dlast[int64_t(walk.seq(m, t0, e)) * p.dl_sb + d * p.dl_sd];
+          set(gv, e, g);
+        }
+        float ca = end ? kResetA : of(a, e), cb = of(a, e) * g;
+        compose<VL>(ca, cb, A, B);
+        A = ca;
+        B = cb;
+      }
+      if (Z) win_store(dz, wt, lane, m.valid, inner, zv);
+      float ck = tile_carry<VL, true, W, CL>(A, B, c, sm, flip, wc, lane, rank, split);
+#pragma unroll
+      for (int e = kGs - 1; e >= 0; --e) {
+        const float g = of(gv, e), se = m.last >> e & 1u ? g : g + ck;
+        ck = of(a, e) * se;
+        if ((m.first >> e & 1u) && p.dh0) p.dh0[int64_t(walk.seq(m, t0, e)) * p.dh_sb + d * p.dh_sd] = ck;
+        set(s, e, m.valid >> e & 1u ? se : 0.0f);  // what flows past the steps outside stays out of the sums
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kH; ++k) {
+      const f2_t ww = mul2(s[k], xv[k]);
+      rv[k] = mul2(rv[k], ww);
+      xv[k] = mul2(s[k], pv[k]);
+      cv[k] = mul2(s[k], cv[k]);
       acc_w = add2(acc_w, ww);
-      acc_r = add2(acc_r, gr);
-      acc_i = add2(acc_i, gi);
-      rv[k] = gr;
-      xv[k] = gx;
-      cv[k] = gi;
+      acc_r = add2(acc_r, rv[k]);
+      acc_i = add2(acc_i, cv[k]);
     }
-    win_store<T, E>(dx, t0, m.valid, vec, xv);
-    win_store<T, E>(dr, t0, m.valid, vec, rv);
-    if (Z) win_store<T, E>(dz, t0, m.valid, vec, zv);
-    win_store<T, E>(di, t0, m.valid, vec, cv);
-    sum_w += f2lo(acc_w) + f2hi(acc_w);
-    sum_r += f2lo(acc_r) + f2hi(acc_r);
-    sum_i += f2lo(acc_i) + f2hi(acc_i);
+    win_store(dx, wt, lane, m.valid, inner, xv);
+    win_store(dr, wt, lane, m.valid, inner, rv);
+    win_store(di, wt, lane, m.valid, inner, cv);
   }
+  float sum_w = f2lo(acc_w) + f2hi(acc_w), sum_r = f2lo(acc_r) + f2hi(acc_r), sum_i = f2lo(acc_i) + f2hi(acc_i);
   if (!VL && p.dh0 && lane == 0 && wr == 0) p.dh0[bt * p.dh_sb + d * p.dh_sd] = c;
 
   // the row's sums, in a fixed order
@@ -1108,20 +1123,18 @@ template <typename T, bool Z>
 __global__ void __launch_bounds__(256) gated_step_kernel(const GatedStepArgs p) {
   const int64_t at = int64_t(blockIdx.x) * 256 + threadIdx.x;
   if (at >= int64_t(p.Bt) * p.D) return;
-  const int bt = int(at / p.D), d = int(at % p.D);
+  const int bt = int(unsigned(at) / unsigned(p.D)), d = int(unsigned(at) % unsigned(p.D));  // Bt D < 2^31
   const GatedRow w = gated_row(p, d);
   float* st = p.state + bt * p.st_sb + d * p.st_sd;
   const float xv = Elem<T>::load(static_cast<const T*>(p.x) + bt * p.x_sb + d * p.x_sd);
   const float rv = Elem<T>::load(static_cast<const T*>(p.r) + bt * p.r_sb + d * p.r_sd);
   const float iv = Elem<T>::load(static_cast<const T*>(p.i) + bt * p.i_sb + d * p.i_sd);
   const float zv = Z ? Elem<T>::load(static_cast<const T*>(p.z) + bt * p.z_sb + d * p.z_sd) : 0.0f;
-  const f2_t x2[1] = {f2s(xv)}, r2[1] = {f2s(rv)}, i2[1] = {f2s(iv)};
-  f2_t z2[1] = {f2s(zv)};
-  float a[2], b[2];
-  steps<Z, true, 2>(x2, r2, i2, z2, w, a, b);  // a gate each: the step waits for memory, not for the SFU
-  const float h = fmaf(a[0], *st, b[0]);
+  f2_t a, b, g = 0, most = 0;
+  step_pair<Z, true>(f2s(xv), f2s(rv), f2s(iv), f2s(zv), w, a, b, g, most);  // waits for memory, not for the SFU
+  const float h = fmaf(f2lo(a), *st, f2lo(b));
   *st = h;
-  const float y = Z ? h * f2lo(z2[0]) : h;
+  const float y = Z ? h * f2lo(g) : h;
   T* o = static_cast<T*>(p.out) + bt * p.o_sb + d * p.o_sd;
   if constexpr (sizeof(T) == 2) *o = f_to_bf16(y);
   else *o = y;

@@ -24,8 +24,8 @@ static __global__ void gated_param_grads_kernel(const GatedArgs p) {
 
 template <typename T, int W, bool Z, bool CL>
 static cudaError_t bwd_v(const GatedArgs& a, size_t smem, cudaStream_t s) {
-  if (a.cu) return gated_launch(gated_bwd_kernel<T, kGs, W, Z, true, CL>, a, W, smem, s);
-  return gated_launch(gated_bwd_kernel<T, kGs, W, Z, false, CL>, a, W, smem, s);
+  if (a.cu) return gated_launch(gated_bwd_kernel<T, W, Z, true, CL>, a, W, smem, s);
+  return gated_launch(gated_bwd_kernel<T, W, Z, false, CL>, a, W, smem, s);
 }
 
 template <typename T, int W, bool CL>
@@ -37,6 +37,7 @@ template <typename T>
 static cudaError_t bwd_t(const GatedArgs& a, int warps, size_t smem, cudaStream_t s) {
   if (a.split > 1) return bwd_w<T, 8, true>(a, smem, s);
   return warps == 1 ? bwd_w<T, 1, false>(a, smem, s)
+         : warps == 2 ? bwd_w<T, 2, false>(a, smem, s)
          : warps == 4 ? bwd_w<T, 4, false>(a, smem, s) : bwd_w<T, 8, false>(a, smem, s);
 }
 

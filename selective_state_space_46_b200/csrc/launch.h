@@ -44,7 +44,7 @@ cudaError_t launch_causal_conv1d_update(const ConvUpdateArgs& a, int dtype, cuda
 // Backward scan: pass A (chunk summaries both ways and their folds, when there is more than
 // one chunk) and pass B (recompute and backward sweep per chunk).
 cudaError_t launch_scan_bwd(const BwdArgs& a, int dtype, bool has_z, cudaStream_t s);
-// Gated linear recurrence: `warps` (1, 4 or 8) warps of a CTA per row, and a.split CTAs (above 1: 8 warps,
+// Gated linear recurrence: `warps` (1, 2, 4 or 8) warps of a CTA per row, and a.split CTAs (above 1: 8 warps,
 // and a cluster).  The backward pass is followed by the sum of the batch's row sums when a.part is given.
 cudaError_t launch_gated_scan(const GatedArgs& a, int warps, int dtype, cudaStream_t s);
 cudaError_t launch_gated_bwd(const GatedArgs& a, int warps, int dtype, cudaStream_t s);

@@ -292,7 +292,7 @@ def test_strides_and_alignment(cuda_device, io, how):
     assert (cat[..., 0] == 5).all() and (cat[..., L + 1:] == 5).all()
 
 
-PLANS = [(1, 1), (4, 1), (8, 1), (8, 2), (8, 4), (8, 8)]
+PLANS = [(1, 1), (2, 1), (4, 1), (8, 1), (8, 2), (8, 4), (8, 8)]
 
 
 @pytest.mark.parametrize("plan", PLANS)
