@@ -1267,6 +1267,7 @@ mssm_status gated_prepare(const mssm_tensor* x, const mssm_tensor* r, const mssm
 //  * as many warps as keep all rows' warps within 70 per SM (three rounds of resident CTAs): 5120x4096
 //    with 1 / 2 / 4 / 8 warps 55 / 51 / 51 / 61 and 131 / 115 / 115 / 133, 1536x16384 76 / 68 / 61 / 66 and
 //    184 / 162 / 143 / 154, 300x32768 104 / 64 / 41 / 39; and no more than the length fills (8192x256: 14 / 23 / 37 / 76);
+//  * two warps for long rows however many there are: 40960x4096 backward with 1 / 2 / 4 warps 866 / 786 / 821;
 //  * a cluster only while its CTAs' warps stay within 14 per SM and each keeps two tiles or more: 16x131072 in
 //    1 / 2 / 4 / 8 CTAs 68 / 68 / 37 / 25, 64x65536 37 / 39 / 25 / 27, but 148x65536 39 / 45 / 49 / 49.
 struct GatedShape {
@@ -1276,7 +1277,9 @@ struct GatedShape {
 GatedShape gated_shape(int64_t rows, int64_t L, int sms) {
   const int64_t step = 32 * mssm::kGs;  // steps of a warp
   GatedShape g{1, 1};
-  while (g.warps < 8 && g.warps * step < L && rows * g.warps * 2 <= int64_t(70) * sms) g.warps *= 2;
+  while (g.warps < 8 && g.warps * step < L &&
+         (rows * g.warps * 2 <= int64_t(70) * sms || (g.warps == 1 && L >= 8 * step)))
+    g.warps *= 2;
   while (g.warps == 8 && g.split < mssm::kMaxSplit && rows * 8 * g.split * 2 <= int64_t(14) * sms &&
          L >= 8 * step * 4 * g.split)
     g.split *= 2;

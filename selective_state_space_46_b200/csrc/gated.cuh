@@ -528,11 +528,13 @@ struct CarrySmem {
 };
 
 // Carries `h` across a tile of W warps (CL: of a cluster's CTAs): in, the value before the tile; out,
-// after it.  a, b: the thread's map.  Returns the value before the thread's own steps.
+// after it.  a, b: the thread's map; whole: the warp's maps hold no reset.  Returns the value before the thread's own
+// steps.
 template <bool VL, bool REV, int W, bool CL>
 __device__ __forceinline__ float tile_carry(float a, float b, float& h, CarrySmem<W>& sm, int& flip, int warp, int lane,
-                                            int rank, int split) {
-  warp_compose<VL, REV>(a, b, lane);
+                                            int rank, int split, bool whole) {
+  if (!VL || whole) warp_compose<false, REV>(a, b, lane);
+  else warp_compose<true, REV>(a, b, lane);
   float ea = REV ? __shfl_down_sync(~0u, a, 1) : __shfl_up_sync(~0u, a, 1);
   float eb = REV ? __shfl_down_sync(~0u, b, 1) : __shfl_up_sync(~0u, b, 1);
   constexpr int edge = REV ? 0 : 31;
@@ -736,7 +738,7 @@ __global__ void __launch_bounds__(gated_threads(W), kScanWarps * 32 / gated_thre
         }
       }
       const WinMap wm = win_map(a, b);
-      const float in = tile_carry<VL, false, W, CL>(wm.A, wm.B, h, sm, flip, at.wc, lane, at.rank, at.split);
+      const float in = tile_carry<VL, false, W, CL>(wm.A, wm.B, h, sm, flip, at.wc, lane, at.rank, at.split, whole);
       f2_t hh = f2(in, fmaf(wm.a_lo, in, wm.b_lo));
 #pragma unroll
       for (int k = 0; k < kH; ++k) {
@@ -762,7 +764,7 @@ __global__ void __launch_bounds__(gated_threads(W), kScanWarps * 32 / gated_thre
         A = ca;
         B = cb;
       }
-      float hk = tile_carry<VL, false, W, CL>(A, B, h, sm, flip, at.wc, lane, at.rank, at.split);
+      float hk = tile_carry<VL, false, W, CL>(A, B, h, sm, flip, at.wc, lane, at.rank, at.split, whole);
 #pragma unroll
       for (int e = 0; e < kGs; ++e) {
         hk = apply<VL>(of(a, e), of(b, e), hk);
@@ -927,7 +929,7 @@ __global__ void __launch_bounds__(gated_threads(W), kBwdWarps * 32 / gated_threa
         B = cb;
       }
     }
-    tile_carry<VL, false, W, CL>(A, B, h, sm, flip, wc, lane, rank, split);
+    tile_carry<VL, false, W, CL>(A, B, h, sm, flip, wc, lane, rank, split, whole);
   }
   if (lane == 0 && wc == 0 && ntiles > 0) ckpt[ntiles - 1] = h;
   if (W == 1) __syncwarp();
@@ -971,7 +973,7 @@ __global__ void __launch_bounds__(gated_threads(W), kBwdWarps * 32 / gated_threa
     float hin = ckpt[tl];
     if (!VL || whole) {
       const WinMap wm = win_map(a, b);
-      const float in = tile_carry<VL, false, W, CL>(wm.A, wm.B, hin, sm, flip, wc, lane, rank, split);
+      const float in = tile_carry<VL, false, W, CL>(wm.A, wm.B, hin, sm, flip, wc, lane, rank, split, whole);
       // w / s = a (i x rho - y h_before), dz, and what flows back out of the halves
       f2_t hh = f2(in, fmaf(wm.a_lo, in, wm.b_lo));
 #pragma unroll
@@ -986,7 +988,7 @@ __global__ void __launch_bounds__(gated_threads(W), kBwdWarps * 32 / gated_threa
       float c_lo, c_hi;
       f2split(back, c_lo, c_hi);
       if (Z) win_store(dz, wt, lane, m.valid, inner, zv);
-      const float cin = tile_carry<VL, true, W, CL>(wm.A, fmaf(wm.a_lo, c_hi, c_lo), c, sm, flip, wc, lane, rank, split);
+      const float cin = tile_carry<VL, true, W, CL>(wm.A, fmaf(wm.a_lo, c_hi, c_lo), c, sm, flip, wc, lane, rank, split, whole);
       f2_t cc = f2(fmaf(wm.a_hi, cin, c_hi), cin);
 #pragma unroll
       for (int k = kH - 1; k >= 0; --k) {
@@ -1008,7 +1010,7 @@ __global__ void __launch_bounds__(gated_threads(W), kBwdWarps * 32 / gated_threa
         A = ca;
         B = cb;
       }
-      float hk = tile_carry<VL, false, W, CL>(A, B, hin, sm, flip, wc, lane, rank, split);
+      float hk = tile_carry<VL, false, W, CL>(A, B, hin, sm, flip, wc, lane, rank, split, whole);
 #pragma unroll
       for (int e = 0; e < kGs; ++e) {
         if (!(m.first >> e & 1u)) hb[e] = hk;
@@ -1038,7 +1040,7 @@ __global__ void __launch_bounds__(gated_threads(W), kBwdWarps * 32 / gated_threa
         B = cb;
       }
       if (Z) win_store(dz, wt, lane, m.valid, inner, zv);
-      float ck = tile_carry<VL, true, W, CL>(A, B, c, sm, flip, wc, lane, rank, split);
+      float ck = tile_carry<VL, true, W, CL>(A, B, c, sm, flip, wc, lane, rank, split, whole);
 #pragma unroll
       for (int e = kGs - 1; e >= 0; --e) {
         const float g = of(gv, e), se = m.last >> e & 1u ? g : g + ck;
