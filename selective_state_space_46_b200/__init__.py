@@ -28,7 +28,7 @@ __all__ = [
     "mssm_selective_scan_fwd_ex", "MSSM_DISC_EULER", "MSSM_DISC_ZOH",
     "mssm_causal_conv1d_fwd", "mssm_causal_conv1d_update", "causal_conv1d", "causal_conv1d_update",
     "mssm_selective_scan_bwd", "selective_scan_bwd",
-    "MSSM_OPT_GATED_WARPS", "MSSM_OPT_GATED_SPLIT", "mssm_gated_scan_fwd", "mssm_gated_scan_bwd", "mssm_gated_state_update",
+    "MSSM_OPT_GATED_WARPS", "MSSM_OPT_GATED_SPLIT", "MSSM_OPT_W4_WARPS", "MSSM_OPT_GATED_STEP_ROWS", "mssm_gated_scan_fwd", "mssm_gated_scan_bwd", "mssm_gated_state_update",
     "gated_scan_fwd", "gated_scan_bwd", "gated_state_update",
     "mssm_w4_pack", "mssm_w4_linear", "W4Weight", "w4_pack", "w4_linear",
     "KERNEL_KINDS",
@@ -40,6 +40,11 @@ if not os.path.exists(lib_path):
     raise ImportError(f"{lib_path} is missing: build it with `python selective_state_space_46_b200/build.py` "
                       "(nvcc, sm_100a); there is no fallback implementation")
 _lib = ctypes.CDLL(lib_path)
+try:
+    from . import _marshal
+except ImportError as e:
+    raise ImportError("the binding's descriptor writer (_marshal.so) is missing or was built for another torch: build it "
+                      "with `python selective_state_space_46_b200/build.py`") from e
 
 MSSM_F32, MSSM_BF16 = 0, 1
 MSSM_OK, MSSM_ERR_INVALID_ARG, MSSM_ERR_UNSUPPORTED, MSSM_ERR_CUDA, MSSM_ERR_TIMEOUT = 0, 1, 2, 3, 4
@@ -48,7 +53,7 @@ MSSM_OPT_DECODE_PATH = 5
 MSSM_OPT_TEST_HOOKS = 6
 MSSM_OPT_ROWS_PER_CTA = 7
 MSSM_OPT_ROWS_PER_THREAD = 8
-MSSM_OPT_GATED_WARPS, MSSM_OPT_GATED_SPLIT = 9, 10
+MSSM_OPT_GATED_WARPS, MSSM_OPT_GATED_SPLIT, MSSM_OPT_W4_WARPS, MSSM_OPT_GATED_STEP_ROWS = 9, 10, 11, 12
 MSSM_DISC_EULER, MSSM_DISC_ZOH = 0, 1
 SCHEDULES = {"forward": 1, "summaries+forward": 2, "chained": 3, "fused": 4, "split": 5}
 DECODE_PATHS = {"stream": 1, "bulk_tile": 2, "per_row": 3}
@@ -309,41 +314,21 @@ def mssm_causal_conv1d_update(conv_state, x, weight, bias, out, silu_flag=True, 
                                           _stream(stream, x)))
 
 
-class _Descs(threading.local):
-    """A thread's block of ``mssm_tensor`` descriptors, written in place: a decode step is a few
-    microseconds on the GPU, so the marshalling of its arguments is kept short."""
+class _Block(threading.local):
+    """A thread's block of ``mssm_tensor`` descriptors, written in place by ``_marshal``, and of one
+    ``mssm_gated_ext`` behind them."""
     MOST = 20
-    LAYOUT = struct.Struct("qii8q")
+    EXT = struct.Struct("ifQQ")  # struct_size, decay_scale, h0, cu_seqlens
 
     def __init__(self):
-        self.block = ctypes.create_string_buffer(self.MOST * ctypes.sizeof(mssm_tensor))
-        self.base = ctypes.addressof(self.block)
+        end = self.MOST * ctypes.sizeof(mssm_tensor)
+        self.buffer = ctypes.create_string_buffer(end + self.EXT.size)
+        self.base = ctypes.addressof(self.buffer)
+        self.ext_at, self.ext = end, self.base + end
 
-    def __call__(self, *tensors):
-        """Descriptor addresses (None for None), valid until the thread's next call."""
-        out = []
-        at, block, pack, base = 0, self.block, self.LAYOUT.pack_into, self.base
-        for t in tensors:
-            if t is None:
-                out.append(None)
-                continue
-            shape, stride = t.shape, t.stride()
-            n = len(shape)
-            if n == 3:
-                pack(block, at, t.data_ptr(), _DT.get(t.dtype, -1), 3, *shape, 0, *stride, 0)
-            elif n == 2:
-                pack(block, at, t.data_ptr(), _DT.get(t.dtype, -1), 2, *shape, 0, 0, *stride, 0, 0)
-            elif n == 1:
-                pack(block, at, t.data_ptr(), _DT.get(t.dtype, -1), 1, shape[0], 0, 0, 0, stride[0], 0, 0, 0)
-            else:
-                raise ValueError("tensors have 1 to 3 dims here")
-            out.append(base + at)
-            at += 80
-        return out
-
-
-assert _Descs.LAYOUT.size == ctypes.sizeof(mssm_tensor) == 80
-_descs = _Descs()
+    def gated_ext(self, decay_scale, h0, cu_seqlens):
+        self.EXT.pack_into(self.buffer, self.ext_at, self.EXT.size, decay_scale, h0 or 0, cu_seqlens or 0)
+        return self.ext
 
 
 class mssm_gated_ext(ctypes.Structure):
@@ -351,25 +336,25 @@ class mssm_gated_ext(ctypes.Structure):
                 ("h0", ctypes.c_void_p), ("cu_seqlens", ctypes.c_void_p)]
 
 
-def _on(stream, x, *tensors):
-    """The raw stream of a call on the tensors' device, which is made current for it."""
-    device = x.device
-    if device.type != "cuda":
-        raise ValueError("this operator runs on CUDA tensors only")
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"all tensors must be on {device} (got one on {t.device})")
+assert ctypes.sizeof(mssm_tensor) == 80 and ctypes.sizeof(mssm_gated_ext) == _Block.EXT.size
+_block = _Block()
+
+
+def _call(stream, device, fn, *args):
+    """A library call on a stream of the tensors' device, which is made current for it."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-
-
-def _call(device, fn, *args):
-    if torch._C._cuda_getDevice() == device.index:
-        _check(fn(*args))
+        stream = torch._C._cuda_getCurrentRawStream(device)
+    elif isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
+    else:
+        stream = int(stream)
+    if torch._C._cuda_getDevice() == device:
+        status = fn(*args, stream)
     else:
         with torch.cuda.device(device):
-            _check(fn(*args))
+            status = fn(*args, stream)
+    if status != MSSM_OK:
+        _check(status)
 
 
 class _allocating_on:
@@ -392,42 +377,36 @@ class _allocating_on:
 def mssm_gated_scan_fwd(x, r, i, lam, r_bias, i_bias, z, out, last_state, decay_scale=8.0, h0=None, cu_seqlens=None,
                         stream=None) -> None:
     """Marshal torch tensors into ``mssm_gated_scan_fwd`` (see include/mssm.h)."""
-    s = _on(stream, x, r, i, lam, r_bias, i_bias, z, out, last_state, h0, cu_seqlens)
-    d = _descs(x, r, i, lam, r_bias, i_bias, z, out, last_state, h0, cu_seqlens)
-    ext = mssm_gated_ext(ctypes.sizeof(mssm_gated_ext), decay_scale, d[9], d[10])
-    _call(x.device, _lib.mssm_gated_scan_fwd, *d[:7], ctypes.addressof(ext), d[7], d[8], s)
+    b = _block
+    dev, *d = _marshal.describe(b.base, x, r, i, lam, r_bias, i_bias, z, out, last_state, h0, cu_seqlens)
+    _call(stream, dev, _lib.mssm_gated_scan_fwd, *d[:7], b.gated_ext(decay_scale, d[9], d[10]), d[7], d[8])
 
 
 def mssm_gated_scan_bwd(x, r, i, lam, r_bias, i_bias, z, dout, dlast_state, dx, dr, di, dz, dlam, dr_bias, di_bias,
-                        dh0, workspace, decay_scale=8.0, h0=None, cu_seqlens=None, stream=None) -> None:
+                        dh0, workspace=None, decay_scale=8.0, h0=None, cu_seqlens=None, stream=None) -> None:
     """Marshal torch tensors into ``mssm_gated_scan_bwd`` (see include/mssm.h)."""
-    ts = (x, r, i, lam, r_bias, i_bias, z, dout, dlast_state, dx, dr, di, dz, dlam, dr_bias, di_bias, dh0, workspace,
-          h0, cu_seqlens)
-    s = _on(stream, *ts)
-    d = _descs(*ts)
-    ext = mssm_gated_ext(ctypes.sizeof(mssm_gated_ext), decay_scale, d[18], d[19])
-    _call(x.device, _lib.mssm_gated_scan_bwd, *d[:7], ctypes.addressof(ext), *d[7:18], s)
+    b = _block
+    dev, *d = _marshal.describe(b.base, x, r, i, lam, r_bias, i_bias, z, dout, dlast_state, dx, dr, di, dz, dlam,
+                                dr_bias, di_bias, dh0, workspace, h0, cu_seqlens)
+    _call(stream, dev, _lib.mssm_gated_scan_bwd, *d[:7], b.gated_ext(decay_scale, d[18], d[19]), *d[7:18])
 
 
 def mssm_gated_state_update(state, x, r, i, lam, r_bias, i_bias, z, out, decay_scale=8.0, stream=None) -> None:
     """Marshal torch tensors into ``mssm_gated_state_update`` (state updated in place)."""
-    s = _on(stream, x, state, r, i, lam, r_bias, i_bias, z, out)
-    d = _descs(state, x, r, i, lam, r_bias, i_bias, z, out)
-    _call(x.device, _lib.mssm_gated_state_update, *d[:8], decay_scale, d[8], s)
+    dev, *d, o = _marshal.describe(_block.base, state, x, r, i, lam, r_bias, i_bias, z, out)
+    _call(stream, dev, _lib.mssm_gated_state_update, *d, decay_scale, o)
 
 
 def mssm_w4_pack(codes, scales, zeros, in_features, group_size, qweight, qscales, qzeros, stream=None) -> None:
     """Marshal torch tensors into ``mssm_w4_pack`` (see include/mssm.h)."""
-    s = _on(stream, codes, scales, zeros, qweight, qscales, qzeros)
-    d = _descs(codes, scales, zeros, qweight, qscales, qzeros)
-    _call(codes.device, _lib.mssm_w4_pack, *d[:3], in_features, group_size, *d[3:], s)
+    dev, *d = _marshal.describe(_block.base, codes, scales, zeros, qweight, qscales, qzeros)
+    _call(stream, dev, _lib.mssm_w4_pack, *d[:3], in_features, group_size, *d[3:])
 
 
 def mssm_w4_linear(x, qweight, qscales, qzeros, group_size, bias, out, stream=None) -> None:
     """Marshal torch tensors into ``mssm_w4_linear`` (see include/mssm.h)."""
-    s = _on(stream, x, qweight, qscales, qzeros, bias, out)
-    d = _descs(x, qweight, qscales, qzeros, bias, out)
-    _call(x.device, _lib.mssm_w4_linear, *d[:4], group_size, d[4], d[5], s)
+    dev, *d, b, o = _marshal.describe(_block.base, x, qweight, qscales, qzeros, bias, out)
+    _call(stream, dev, _lib.mssm_w4_linear, *d, group_size, b, o)
 
 
 # --------------------------------------------------------------------------

@@ -7,7 +7,8 @@ would load the library it is meant to build.
 
 Each .cu file is compiled to an object in parallel, then linked into a shared
 library next to this file.  The CUDA runtime is linked statically, so loading
-the library needs no GPU (only calling into it does).
+the library needs no GPU (only calling into it does).  The Python binding's
+descriptor writer (csrc/marshal.cpp) becomes _marshal.so beside it.
 """
 from __future__ import annotations
 
@@ -24,6 +25,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmssm.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
+MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", *ARCH,
@@ -46,6 +49,28 @@ def _inputs():
         + [os.path.join(INCLUDE, "mssm.h"), os.path.abspath(__file__)]
 
 
+def build_marshal(force: bool = False, verbose: bool = False) -> str:
+    """The binding's descriptor writer: a CPython extension against the installed torch's headers."""
+    import sysconfig
+    import torch
+    base = os.path.dirname(os.path.abspath(torch.__file__))
+    inputs = [MARSHAL_SRC, os.path.join(INCLUDE, "mssm.h"), os.path.abspath(__file__), os.path.join(base, "version.py")]
+    if not force and os.path.exists(MARSHAL) and all(os.path.getmtime(p) <= os.path.getmtime(MARSHAL) for p in inputs):
+        return MARSHAL
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", f"-I{INCLUDE}", f"-I{base}/include",
+           f"-I{base}/include/torch/csrc/api/include", f"-I{sysconfig.get_paths()['include']}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", MARSHAL_SRC, "-o", tmp,
+           f"-L{base}/lib", "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"building _marshal.so failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def up_to_date() -> bool:
     if not os.path.exists(LIB):
         return False
@@ -54,6 +79,7 @@ def up_to_date() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
+    build_marshal(force, verbose)
     if not force and up_to_date():
         return LIB
     nvcc = _nvcc()

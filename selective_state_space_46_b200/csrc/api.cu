@@ -41,6 +41,8 @@ int g_rows_per_thread = 0;  // 0 automatic, else 1 or 2
 int g_decode_path = 0;  // MSSM_OPT_DECODE_PATH
 int g_gated_warps = 0;  // MSSM_OPT_GATED_WARPS
 int g_gated_split = 0;  // MSSM_OPT_GATED_SPLIT
+int g_w4_warps = 0;     // MSSM_OPT_W4_WARPS
+int g_step_rows = 0;    // MSSM_OPT_GATED_STEP_ROWS
 int g_test_hooks = 0;   // MSSM_OPT_TEST_HOOKS  // -1 automatic, else the forced LaunchShape mode
 
 // ---- launch accounting and optional per-kernel event timing (diagnostics)
@@ -389,6 +391,16 @@ mssm_status mssm_set_option(int option, int64_t value) {
       if (value != 0 && value != 1 && value != 2 && value != 4 && value != 8)
         return fail(MSSM_ERR_INVALID_ARG, "GATED_SPLIT takes 0, 1, 2, 4 or 8");
       g_gated_split = int(value);
+      return MSSM_OK;
+    case MSSM_OPT_GATED_STEP_ROWS:
+      if (value != 0 && value != 1 && value != 2 && value != 4)
+        return fail(MSSM_ERR_INVALID_ARG, "GATED_STEP_ROWS takes 0, 1, 2 or 4");
+      g_step_rows = int(value);
+      return MSSM_OK;
+    case MSSM_OPT_W4_WARPS:
+      if (value != 0 && value != 4 && value != 8 && value != 16)
+        return fail(MSSM_ERR_INVALID_ARG, "W4_WARPS takes 0, 4, 8 or 16");
+      g_w4_warps = int(value);
       return MSSM_OK;
     case MSSM_OPT_KERNEL_TIMING:
       if (value != 0 && value != 1) return fail(MSSM_ERR_INVALID_ARG, "KERNEL_TIMING takes 0 or 1");
@@ -1437,7 +1449,17 @@ mssm_status mssm_gated_state_update(mssm_tensor* state, const mssm_tensor* x, co
   a.Bt = int(Bt); a.D = int(Dd);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   std::lock_guard<std::mutex> lk(g_mu);
-  cudaError_t e = tracked(MSSM_KERNEL_GATED_STEP, s, [&] { return mssm::launch_gated_step(a, dt, s); });
+  bool vec = Dd % 4 == 0;
+  for (const mssm_tensor* t : {static_cast<const mssm_tensor*>(state), x, r, i, z, static_cast<const mssm_tensor*>(out)})
+    if (t)
+      vec &= (t->stride[1] == 1 || Dd == 1) && (Bt == 1 || t->stride[0] % 4 == 0) &&
+             reinterpret_cast<uintptr_t>(t->data) % (4 * size_t(esize(t->dtype))) == 0;
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  const int64_t per = vec ? Dd / 4 : Dd, want = int64_t(device_state(dev)->sm_count) * 512;
+  const int rows = g_step_rows ? g_step_rows : Bt >= 4 && per * Bt / 4 >= want ? 4 : Bt >= 2 && per * Bt / 2 >= want ? 2 : 1;
+  e = tracked(MSSM_KERNEL_GATED_STEP, s, [&] { return mssm::launch_gated_step(a, vec, rows, dt, s); });
   if (e != cudaSuccess) return cuda_fail(e, "gated state update launch");
   return MSSM_OK;
 }
@@ -1553,10 +1575,14 @@ mssm_status mssm_w4_linear(const mssm_tensor* x, const mssm_tensor* qweight, con
   a.out = out->data; a.o_sm = out->stride[0]; a.o_sn = out->stride[1];
   a.M = int(M); a.N = int(N); a.K = int(K);
   a.blocks = int(w.blocks); a.groups = int(w.groups); a.group = int(group);
+  a.group_shift = -1;
+  for (int k = 0; k < 26; ++k)
+    if ((int64_t(32) << k) == group) a.group_shift = k;
   a.vec_x = aligned16(x->data) && (M == 1 || (x->stride[0] * int64_t(esize(dt))) % 16 == 0);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   std::lock_guard<std::mutex> lk(g_mu);
-  cudaError_t e = tracked(MSSM_KERNEL_W4_LINEAR, s, [&] { return mssm::launch_w4_linear(a, dt, qscales->dtype, s); });
+  const int warps = g_w4_warps ? g_w4_warps : 8;
+  cudaError_t e = tracked(MSSM_KERNEL_W4_LINEAR, s, [&] { return mssm::launch_w4_linear(a, warps, dt, qscales->dtype, s); });
   if (e != cudaSuccess) return cuda_fail(e, "4-bit linear launch");
   return MSSM_OK;
 }

@@ -26,18 +26,25 @@ cudaError_t launch_gated_scan(const GatedArgs& a, int warps, int dtype, cudaStre
   return dtype == 1 ? scan_t<uint16_t>(a, warps, s) : scan_t<float>(a, warps, s);
 }
 
-template <typename T>
-static cudaError_t step_t(const GatedStepArgs& a, cudaStream_t s) {
-  const unsigned g = unsigned((int64_t(a.Bt) * a.D + 255) / 256);
+template <typename T, int V, int R>
+static cudaError_t step_r(const GatedStepArgs& a, cudaStream_t s) {
+  const int64_t n = int64_t((a.D + V - 1) / V) * ((a.Bt + R - 1) / R);
+  const unsigned g = unsigned((n + kStepThreads - 1) / kStepThreads);
   if (a.z)
-    gated_step_kernel<T, true><<<g, 256, 0, s>>>(a);
+    gated_step_kernel<T, V, R, true><<<g, kStepThreads, 0, s>>>(a);
   else
-    gated_step_kernel<T, false><<<g, 256, 0, s>>>(a);
+    gated_step_kernel<T, V, R, false><<<g, kStepThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
-cudaError_t launch_gated_step(const GatedStepArgs& a, int dtype, cudaStream_t s) {
-  return dtype == 1 ? step_t<uint16_t>(a, s) : step_t<float>(a, s);
+template <typename T>
+static cudaError_t step_t(const GatedStepArgs& a, bool vec, int rows, cudaStream_t s) {
+  if (!vec) return rows > 1 ? step_r<T, 1, 4>(a, s) : step_r<T, 1, 1>(a, s);
+  return rows > 2 ? step_r<T, 4, 4>(a, s) : rows > 1 ? step_r<T, 4, 2>(a, s) : step_r<T, 4, 1>(a, s);
+}
+
+cudaError_t launch_gated_step(const GatedStepArgs& a, bool vec, int rows, int dtype, cudaStream_t s) {
+  return dtype == 1 ? step_t<uint16_t>(a, vec, rows, s) : step_t<float>(a, vec, rows, s);
 }
 
 }  // namespace mssm

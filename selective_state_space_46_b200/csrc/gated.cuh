@@ -20,6 +20,7 @@
 namespace mssm {
 
 constexpr int kGs = 8;             // steps per thread
+constexpr int kStepThreads = 128;  // of a CTA of the decode step
 constexpr float kResetA = -0.0f;   // the decay of a sequence's first step: composes to "ignore what came before"
 
 struct GatedArgs {
@@ -206,18 +207,24 @@ __device__ __forceinline__ void decay_care(f2_t y, f2_t& a, f2_t& beta, f2_t& y_
   y_beta = mul2(mul2(y, f2s(kVScale)), q);
 }
 
+// CARE: two steps' a, driven terms b = sqrt(1 - a^2) i x and, with Z, silu(z), from the gates' exponents
+template <bool Z>
+__device__ __forceinline__ void step_care(f2_t x, f2_t ur, f2_t ui, f2_t zz, f2_t rate, f2_t& a, f2_t& b, f2_t& g) {
+  f2_t beta, unused;
+  decay_care(mul2(rcp_2(one_plus(ex2_2(ur))), rate), a, beta, unused);
+  b = mul2(mul2(beta, rcp_2(one_plus(ex2_2(ui)))), x);
+  if (Z) g = mul2(zz, rcp_2(one_plus(ex2_2(mul2(zz, f2s(-kLog2e))))));
+}
+
 // Two steps' a, driven terms b = sqrt(1 - a^2) i x and, with Z, silu(z).
 template <bool Z, bool CARE>
 __device__ __forceinline__ void step_pair(f2_t x, f2_t rr, f2_t ii, f2_t zz, const GatedRow& w, f2_t& a, f2_t& b, f2_t& g,
                                           f2_t& most) {
-  const f2_t er = ex2_2(fma2(rr, f2s(-kLog2e), f2s(w.cr))), ei = ex2_2(fma2(ii, f2s(-kLog2e), f2s(w.ci)));
-  const f2_t ez = Z ? ex2_2(mul2(zz, f2s(-kLog2e))) : 0, pi = one_plus(ei);
+  const f2_t ur = fma2(rr, f2s(-kLog2e), f2s(w.cr)), ui = fma2(ii, f2s(-kLog2e), f2s(w.ci));
   if constexpr (CARE) {
-    f2_t beta, unused;
-    decay_care(mul2(rcp_2(one_plus(er)), f2s(w.rate)), a, beta, unused);
-    b = mul2(mul2(beta, rcp_2(pi)), x);
-    if (Z) g = mul2(zz, rcp_2(one_plus(ez)));
+    step_care<Z>(x, ur, ui, zz, f2s(w.rate), a, b, g);
   } else {
+    const f2_t er = ex2_2(ur), ei = ex2_2(ui), ez = Z ? ex2_2(mul2(zz, f2s(-kLog2e))) : 0, pi = one_plus(ei);
     const f2_t t = Z ? fma2(pi, ez, pi) : pi, tt = mul2(t, t), all = fma2(tt, er, tt);
     most = add2(most, all);
     const f2_t u = rsqrt_2(all), s = mul2(u, t), r = mul2(s, s);
@@ -1121,25 +1128,80 @@ __global__ void __launch_bounds__(gated_threads(W), kBwdWarps * 32 / gated_threa
 
 // ---------------------------------------------------------------- decode step
 
-template <typename T, bool Z>
-__global__ void __launch_bounds__(256) gated_step_kernel(const GatedStepArgs p) {
-  const int64_t at = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (at >= int64_t(p.Bt) * p.D) return;
-  const int bt = int(unsigned(at) / unsigned(p.D)), d = int(unsigned(at) % unsigned(p.D));  // Bt D < 2^31
-  const GatedRow w = gated_row(p, d);
-  float* st = p.state + bt * p.st_sb + d * p.st_sd;
-  const float xv = Elem<T>::load(static_cast<const T*>(p.x) + bt * p.x_sb + d * p.x_sd);
-  const float rv = Elem<T>::load(static_cast<const T*>(p.r) + bt * p.r_sb + d * p.r_sd);
-  const float iv = Elem<T>::load(static_cast<const T*>(p.i) + bt * p.i_sb + d * p.i_sd);
-  const float zv = Z ? Elem<T>::load(static_cast<const T*>(p.z) + bt * p.z_sb + d * p.z_sd) : 0.0f;
-  f2_t a, b, g = 0, most = 0;
-  step_pair<Z, true>(f2s(xv), f2s(rv), f2s(iv), f2s(zv), w, a, b, g, most);  // waits for memory, not for the SFU
-  const float h = fmaf(f2lo(a), *st, f2lo(b));
-  *st = h;
-  const float y = Z ? h * f2lo(g) : h;
-  T* o = static_cast<T*>(p.out) + bt * p.o_sb + d * p.o_sd;
-  if constexpr (sizeof(T) == 2) *o = f_to_bf16(y);
-  else *o = y;
+// A thread takes V neighbouring channels of R batch rows: the channels' constants (a softplus each) once, then
+// all R rows' loads before the first is used.  V = 4 when every row starts on a boundary of 4 elements and
+// channels are next to each other, V = 1 otherwise.
+template <typename T, int V>
+__device__ __forceinline__ void step_load(const T* at, float (&v)[V]) {
+  if constexpr (V == 1) {
+    v[0] = Elem<T>::load(at);
+  } else if constexpr (sizeof(T) == 2) {
+    const uint2 u = *reinterpret_cast<const uint2*>(at);
+    v[0] = bf16lo(u.x); v[1] = bf16hi(u.x); v[2] = bf16lo(u.y); v[3] = bf16hi(u.y);
+  } else {
+    const float4 u = *reinterpret_cast<const float4*>(at);
+    v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void step_store(T* at, const float (&v)[V]) {
+  if constexpr (V == 1) {
+    if constexpr (sizeof(T) == 2) *at = f_to_bf16(v[0]);
+    else *at = v[0];
+  } else if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<uint2*>(at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  } else {
+    *reinterpret_cast<float4*>(at) = make_float4(v[0], v[1], v[2], v[3]);
+  }
+}
+
+template <typename T, int V, int R, bool Z>
+__global__ void __launch_bounds__(kStepThreads) gated_step_kernel(const GatedStepArgs p) {
+  const int per = (p.D + V - 1) / V;  // threads along the channels
+  const unsigned at = blockIdx.x * unsigned(kStepThreads) + threadIdx.x;
+  const int d = int(at % unsigned(per)) * V, b0 = int(at / unsigned(per)) * R;
+  if (b0 >= p.Bt) return;
+  float st[R][V], xv[R][V], rv[R][V], iv[R][V], zv[R][V];
+  const int64_t b64 = b0;
+  float* state = p.state + b64 * p.st_sb + d * p.st_sd;
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    if (b0 + k >= p.Bt) break;
+    const int64_t b = b64 + k;
+    step_load<float, V>(state + k * p.st_sb, st[k]);
+    step_load<T, V>(static_cast<const T*>(p.x) + b * p.x_sb + d * p.x_sd, xv[k]);
+    step_load<T, V>(static_cast<const T*>(p.r) + b * p.r_sb + d * p.r_sd, rv[k]);
+    step_load<T, V>(static_cast<const T*>(p.i) + b * p.i_sb + d * p.i_sd, iv[k]);
+    if (Z) step_load<T, V>(static_cast<const T*>(p.z) + b * p.z_sb + d * p.z_sd, zv[k]);
+  }
+  f2_t rate[(V + 1) / 2], cr[(V + 1) / 2], ci[(V + 1) / 2];
+#pragma unroll
+  for (int v = 0; v < V; v += 2) {
+    const int e = d + (V > 1 ? v + 1 : 0);
+    rate[v / 2] = f2(p.c * softplus_exact(p.lam[(d + v) * p.lam_s]), V > 1 ? p.c * softplus_exact(p.lam[e * p.lam_s]) : 0.0f);
+    cr[v / 2] = p.rb ? mul2(f2s(-kLog2e), f2(p.rb[(d + v) * p.rb_s], p.rb[e * p.rb_s])) : 0;
+    ci[v / 2] = p.ib ? mul2(f2s(-kLog2e), f2(p.ib[(d + v) * p.ib_s], p.ib[e * p.ib_s])) : 0;
+  }
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    if (b0 + k >= p.Bt) break;
+    const int64_t b = b64 + k;
+    float h[V], y[V];
+#pragma unroll
+    for (int v = 0; v < V; v += 2) {
+      constexpr int n = V > 1 ? 1 : 0;
+      const f2_t zz = Z ? f2(zv[k][v], zv[k][v + n]) : 0;
+      f2_t a, bb, g = 0;
+      step_care<Z>(f2(xv[k][v], xv[k][v + n]), fma2(f2(rv[k][v], rv[k][v + n]), f2s(-kLog2e), cr[v / 2]),
+                   fma2(f2(iv[k][v], iv[k][v + n]), f2s(-kLog2e), ci[v / 2]), zz, rate[v / 2], a, bb, g);
+      const f2_t hh = fma2(a, f2(st[k][v], st[k][v + n]), bb), yy = Z ? mul2(hh, g) : hh;
+      h[v] = f2lo(hh);
+      y[v] = f2lo(yy);
+      if (V > 1) h[v + n] = f2hi(hh), y[v + n] = f2hi(yy);
+    }
+    step_store<float, V>(state + k * p.st_sb, h);
+    step_store<T, V>(static_cast<T*>(p.out) + b * p.o_sb + d * p.o_sd, y);
+  }
 }
 
 // ---------------------------------------------------------------- launch

@@ -20,7 +20,6 @@ namespace mssm {
 
 constexpr int kW4Rows = 16;    // outputs per tile
 constexpr int kW4K = 64;       // inputs per block
-constexpr int kW4Warps = 8;    // warps per CTA; they split the inputs
 
 struct W4Args {
   const void* x;               // [M, K], k stride 1
@@ -34,6 +33,7 @@ struct W4Args {
   int64_t o_sm, o_sn;
   int M, N, K;
   int blocks, groups, group;   // blocks of 64 inputs; groups stored per tile; inputs per group
+  int group_shift;             // log2(group / 32), or -1 when the group is no power of two
   bool vec_x;                  // rows of x start on 16-byte boundaries
 };
 
@@ -124,29 +124,17 @@ __device__ __forceinline__ void split3(float x, uint32_t& a, uint32_t& b, uint32
   c = __float_as_uint(r2) >> 16;
 }
 
+// the 8 inputs of a lane, from its places in shared memory (512 bytes apart) in pieces of 16 bytes
 template <typename T>
-__device__ __forceinline__ XFrag<T> x_load(const T* x, int k, int K, bool on, bool vec) {
+__device__ __forceinline__ XFrag<T> x_frag(const char* at) {
   XFrag<T> f;
+  const uint4 u = *reinterpret_cast<const uint4*>(at);
   if constexpr (sizeof(T) == 2) {
-    if (on && vec && k + 8 <= K) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(x + k));
-      f.v[0][0] = u.x; f.v[0][1] = u.y; f.v[0][2] = u.z; f.v[0][3] = u.w;
-      return f;
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t lo = on && k + 2 * j < K ? x[k + 2 * j] : 0u, hi = on && k + 2 * j + 1 < K ? x[k + 2 * j + 1] : 0u;
-      f.v[0][j] = lo | hi << 16;
-    }
+    f.v[0][0] = u.x; f.v[0][1] = u.y; f.v[0][2] = u.z; f.v[0][3] = u.w;
   } else {
-    float e[8];
-    if (on && vec && k + 8 <= K) {
-      const float4 u = __ldg(reinterpret_cast<const float4*>(x + k)), v = __ldg(reinterpret_cast<const float4*>(x + k) + 1);
-      e[0] = u.x; e[1] = u.y; e[2] = u.z; e[3] = u.w; e[4] = v.x; e[5] = v.y; e[6] = v.z; e[7] = v.w;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) e[j] = on && k + j < K ? x[k + j] : 0.0f;
-    }
+    const uint4 v = *reinterpret_cast<const uint4*>(at + 512);
+    const float e[8] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w),
+                        __uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w)};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       uint32_t a0, b0, c0, a1, b1, c1;
@@ -160,25 +148,80 @@ __device__ __forceinline__ XFrag<T> x_load(const T* x, int k, int K, bool on, bo
   return f;
 }
 
-__device__ __forceinline__ float2 load_scale2(const float* s, int64_t at) {
-  return __ldg(reinterpret_cast<const float2*>(s) + at);
-}
-__device__ __forceinline__ float2 load_scale2(const uint16_t* s, int64_t at) {
-  const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(s) + at);
+// The scales of outputs g and g + 8 are a pair of 4 or 8 bytes, read as fp32.
+__device__ __forceinline__ float2 scale_pair(const float* s) { return *reinterpret_cast<const float2*>(s); }
+__device__ __forceinline__ float2 scale_pair(const uint16_t* s) {
+  const uint32_t u = *reinterpret_cast<const uint32_t*>(s);
   return make_float2(bf16lo(u), bf16hi(u));
 }
 
-// One CTA per 16 outputs and 8 * NT tokens; its warps take every kW4Warps-th block of 64 inputs and add up
-// in shared memory, in order.  HALF: the group is an odd multiple of 32, so both halves of a block have
-// their own scale.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(unsigned to, const void* from) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(BYTES) : "memory");
+}
+
+// Asks for 8 inputs of a token from k on (zeros behind the last one).  Rows off a 16-byte boundary: fp32 by the
+// element, bf16 through registers.
+template <typename T>
+__device__ __forceinline__ void x_ask(char* to, const T* x, int k, int K, bool vec) {
+  constexpr int kPiece = 16 / int(sizeof(T));
+  const unsigned at = unsigned(__cvta_generic_to_shared(to));
+#pragma unroll
+  for (int v = 0; v < 8 / kPiece; ++v) {
+    const int k0 = k + v * kPiece, n = max(min(K - k0, kPiece), 0);
+    if (vec) {
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(at + v * 512), "l"(x + (n ? k0 : 0)),
+                   "r"(n * int(sizeof(T)))
+                   : "memory");
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int j = 0; j < kPiece; ++j)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(at + v * 512 + 4 * j), "l"(x + (j < n ? k0 + j : 0)),
+                     "r"(j < n ? 4 : 0)
+                     : "memory");
+    } else {
+      uint32_t u[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        u[j] = (2 * j < n ? uint32_t(x[k0 + 2 * j]) : 0u) | (2 * j + 1 < n ? uint32_t(x[k0 + 2 * j + 1]) << 16 : 0u);
+      *reinterpret_cast<uint4*>(to) = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+  }
+}
+
+// One CTA per 16 outputs and 8 * NT tokens; its W warps take every W-th block of 64 inputs and add up in shared
+// memory, in order.  HALF: the group is an odd multiple of 32, so both halves of a block have their own
+// scale.  The stream of weights is what bounds a few tokens: every lane has its 16 bytes of the next blocks,
+// their scales and its x on the way into its own places of shared memory (no other lane reads them, so the
+// copies' own order is all the synchronisation).
+
 template <typename T, typename S, int NT, bool HALF, bool ZERO>
-__global__ void __launch_bounds__(32 * kW4Warps) w4_linear_kernel(const W4Args p) {
-  __shared__ float s_acc[kW4Warps][NT * 8][kW4Rows + 1];
+struct W4Ring {
+  static constexpr int kSets = HALF ? 2 : 1;
+  static constexpr int kPair = 2 * int(sizeof(S));
+  static constexpr int kXPart = 32 * 8 * int(sizeof(T));  // of half a block and 8 tokens
+  static constexpr int kX = 512, kScale = kX + 2 * NT * kXPart, kZero = kScale + 32 * kPair * kSets;  // places in a slot
+  static constexpr int kSlot = kZero + (ZERO ? 32 * 4 * kSets : 0);
+  // about 7 KB of a warp, so that 32 warps of an SM have 48 KB of weights on the way
+  static constexpr int kSlots = 7168 / kSlot > 6 ? 6 : 7168 / kSlot < 2 ? 2 : 7168 / kSlot;
+  static constexpr int kWarp = kSlot * kSlots;
+};
+
+template <typename T, typename S, int NT, int W, bool HALF, bool ZERO>
+__global__ void __launch_bounds__(32 * W) w4_linear_kernel(const W4Args p) {
+  using Ring = W4Ring<T, S, NT, HALF, ZERO>;
+  constexpr int kSlots = Ring::kSlots;
+  extern __shared__ __align__(16) char s_mem[];  // the warps' rings, then their sums
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, c = lane % 4;
   const int tile = blockIdx.x, m0 = blockIdx.y * (8 * NT);
   const uint4* q = p.q + int64_t(tile) * p.blocks * 32 + lane;
-  const S* scale = static_cast<const S*>(p.scale);
-  const int64_t sbase = int64_t(tile) * p.groups * 8 + g;
+  const S* scale = static_cast<const S*>(p.scale) + (int64_t(tile) * p.groups * 8 + g) * 2;
+  const uint8_t* zero = ZERO ? p.zero + (int64_t(tile) * p.groups * 8 + (g & ~1)) * 2 : nullptr;  // 4 bytes: g and g ^ 1
+  char* ring = s_mem + warp * Ring::kWarp;
+  const unsigned ring_at = unsigned(__cvta_generic_to_shared(ring));
   const T* xr[NT];
   bool on[NT];
 #pragma unroll
@@ -187,46 +230,78 @@ __global__ void __launch_bounds__(32 * kW4Warps) w4_linear_kernel(const W4Args p
     on[n] = m < p.M;
     xr[n] = static_cast<const T*>(p.x) + (on[n] ? m : 0) * p.x_sm;
   }
+  auto ask = [&](int slot, int kb) {
+    if (kb < p.blocks) {
+      const unsigned to = ring_at + slot * Ring::kSlot;
+      copy_async<16>(to + lane * 16, q + int64_t(kb) * 32);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        if (on[n])
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            x_ask(ring + slot * Ring::kSlot + Ring::kX + (2 * n + h) * Ring::kXPart + lane * 16, xr[n],
+                  kb * kW4K + 32 * h + 8 * c, p.K, p.vec_x);
+#pragma unroll
+      for (int h = 0; h < Ring::kSets; ++h) {
+        const unsigned u = unsigned(2 * kb + h);  // in units of 32 inputs
+        const unsigned grp = p.group_shift >= 0 ? u >> p.group_shift : u / unsigned(p.group / 32);
+        copy_async<Ring::kPair>(to + Ring::kScale + (32 * h + lane) * Ring::kPair, scale + size_t(grp) * 16);
+        if (ZERO) copy_async<4>(to + Ring::kZero + (32 * h + lane) * 4, zero + size_t(grp) * 16);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int j = 0; j < kSlots - 1; ++j) ask(j, warp + j * W);
+
   float acc[NT][4];
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int k = 0; k < 4; ++k) acc[n][k] = 0.0f;
 
-  for (int kb = warp; kb < p.blocks; kb += kW4Warps) {
-    const uint4 w = __ldg(q + int64_t(kb) * 32);
+  int slot = 0;
+  for (int kb = warp; kb < p.blocks; kb += W) {
+    ask(slot == 0 ? kSlots - 1 : slot - 1, kb + (kSlots - 1) * W);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 1) : "memory");
+    const char* at = ring + slot * Ring::kSlot;
+    const uint4 w = *reinterpret_cast<const uint4*>(at + lane * 16);
     const uint32_t wlo[2] = {w.x, w.y}, whi[2] = {w.z, w.w};
     float part[NT][4];
-    float2 sc;
     uint32_t z0 = 0x43084308u, z1 = 0x43084308u;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      const int set = HALF ? h : 0;
       if (h == 0 || HALF) {
-        const int grp = (kb * kW4K + 32 * h) / p.group;
-        sc = load_scale2(scale, sbase + int64_t(grp) * 8);
         if (ZERO) {
-          const uint32_t zz = __ldg(reinterpret_cast<const uint16_t*>(p.zero) + sbase + int64_t(grp) * 8);
+          const uint32_t zz = *reinterpret_cast<const uint32_t*>(at + Ring::kZero + (32 * set + lane) * 4) >> (16 * (g & 1));
           z0 = (zz & 0xffu) * 0x10001u | 0x43004300u;
-          z1 = (zz >> 8) * 0x10001u | 0x43004300u;
+          z1 = (zz >> 8 & 0xffu) * 0x10001u | 0x43004300u;
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int k = 0; k < 4; ++k) part[n][k] = 0.0f;
       }
-      XFrag<T> xf[NT];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) xf[n] = x_load(xr[n], kb * kW4K + 32 * h + 8 * c, p.K, on[n], p.vec_x);
+      uint32_t a[2][4];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const uint32_t a[4] = {w4_pair(wlo[h], 2 * s, z0), w4_pair(whi[h], 2 * s, z1), w4_pair(wlo[h], 2 * s + 1, z0),
-                               w4_pair(whi[h], 2 * s + 1, z1)};
+        a[s][0] = w4_pair(wlo[h], 2 * s, z0);
+        a[s][1] = w4_pair(whi[h], 2 * s, z1);
+        a[s][2] = w4_pair(wlo[h], 2 * s + 1, z0);
+        a[s][3] = w4_pair(whi[h], 2 * s + 1, z1);
+      }
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n) {
+        XFrag<T> xf{};
+        if (on[n]) xf = x_frag<T>(at + Ring::kX + (2 * n + h) * Ring::kXPart + lane * 16);
 #pragma unroll
-          for (int t = 0; t < XFrag<T>::kParts; ++t) mma_bf16(part[n], a, xf[n].v[t][2 * s], xf[n].v[t][2 * s + 1]);
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int t = 0; t < XFrag<T>::kParts; ++t) mma_bf16(part[n], a[s], xf.v[t][2 * s], xf.v[t][2 * s + 1]);
       }
       if (h == 1 || HALF) {
+        const float2 sc = scale_pair(reinterpret_cast<const S*>(at + Ring::kScale + (32 * set + lane) * Ring::kPair));
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           acc[n][0] = fmaf(sc.x, part[n][0], acc[n][0]);
@@ -236,25 +311,37 @@ __global__ void __launch_bounds__(32 * kW4Warps) w4_linear_kernel(const W4Args p
         }
       }
     }
+    slot = slot + 1 == kSlots ? 0 : slot + 1;
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
   // accumulator element: rows g (0, 1) and g + 8 (2, 3), tokens 2c and 2c + 1
+  float* s_acc = reinterpret_cast<float*>(s_mem);  // [W][8 NT][kW4Rows + 1]
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) s_acc[warp][8 * n + 2 * c + (k & 1)][g + 8 * (k >> 1)] = acc[n][k];
+    for (int k = 0; k < 4; ++k)
+      s_acc[(warp * 8 * NT + 8 * n + 2 * c + (k & 1)) * (kW4Rows + 1) + g + 8 * (k >> 1)] = acc[n][k];
   __syncthreads();
-  for (int e = threadIdx.x; e < 8 * NT * kW4Rows; e += 32 * kW4Warps) {
+  for (int e = threadIdx.x; e < 8 * NT * kW4Rows; e += 32 * W) {
     const int m = e / kW4Rows, r = e % kW4Rows;
     const int n = tile * kW4Rows + r;
     if (m0 + m >= p.M || n >= p.N) continue;
     float v = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kW4Warps; ++k) v += s_acc[k][m][r];
+    for (int k = 0; k < W; ++k) v += s_acc[(k * 8 * NT + m) * (kW4Rows + 1) + r];
     if (p.bias) v += p.bias[n * p.bias_s];
     T* o = static_cast<T*>(p.out) + (m0 + m) * p.o_sm + n * p.o_sn;
     if constexpr (sizeof(T) == 2) *o = f_to_bf16(v);
     else *o = v;
   }
+}
+
+// shared memory of a CTA
+template <typename T, typename S, int NT, int W, bool HALF, bool ZERO>
+constexpr size_t w4_smem() {
+  const size_t ring = size_t(W) * W4Ring<T, S, NT, HALF, ZERO>::kWarp, sums = size_t(W) * 8 * NT * (kW4Rows + 1) * 4;
+  return ring > sums ? ring : sums;
 }
 
 }  // namespace mssm
