@@ -470,8 +470,8 @@ mssm_status mssm_get_error(void *stream);
  *     gated scans; 0 automatic.
  *   MSSM_OPT_GATED_SPLIT (value 0, 1, 2, 4 or 8): CTAs (a cluster, of 8 warps each) that
  *     share a row of the gated scans; 0 automatic.
- *   MSSM_OPT_W4_WARPS (value 0, 4, 8 or 16): warps of a CTA of the 4-bit linear map, which split
- *     its inputs; 0 automatic.
+ *   MSSM_OPT_W4_PLAN (value 0, 2, 8 or 16): a CTA of the 4-bit linear map takes 32 outputs with 8
+ *     warps (2) or 16 outputs with 8 or 16 warps, which split its inputs; 0 automatic.
  *   MSSM_OPT_GATED_STEP_ROWS (value 0, 1, 2 or 4): batch rows that a thread of the gated state
  *     update takes; 0 automatic.
  * Unknown options or invalid values return MSSM_ERR_INVALID_ARG.
@@ -487,7 +487,7 @@ typedef enum {
     MSSM_OPT_ROWS_PER_THREAD = 8,
     MSSM_OPT_GATED_WARPS = 9,
     MSSM_OPT_GATED_SPLIT = 10,
-    MSSM_OPT_W4_WARPS = 11,
+    MSSM_OPT_W4_PLAN = 11,
     MSSM_OPT_GATED_STEP_ROWS = 12
 } mssm_option;
 mssm_status mssm_set_option(int option, int64_t value);

@@ -28,7 +28,7 @@ __all__ = [
     "mssm_selective_scan_fwd_ex", "MSSM_DISC_EULER", "MSSM_DISC_ZOH",
     "mssm_causal_conv1d_fwd", "mssm_causal_conv1d_update", "causal_conv1d", "causal_conv1d_update",
     "mssm_selective_scan_bwd", "selective_scan_bwd",
-    "MSSM_OPT_GATED_WARPS", "MSSM_OPT_GATED_SPLIT", "MSSM_OPT_W4_WARPS", "MSSM_OPT_GATED_STEP_ROWS", "mssm_gated_scan_fwd", "mssm_gated_scan_bwd", "mssm_gated_state_update",
+    "MSSM_OPT_GATED_WARPS", "MSSM_OPT_GATED_SPLIT", "MSSM_OPT_W4_PLAN", "MSSM_OPT_GATED_STEP_ROWS", "mssm_gated_scan_fwd", "mssm_gated_scan_bwd", "mssm_gated_state_update",
     "gated_scan_fwd", "gated_scan_bwd", "gated_state_update",
     "mssm_w4_pack", "mssm_w4_linear", "W4Weight", "w4_pack", "w4_linear",
     "KERNEL_KINDS",
@@ -53,7 +53,7 @@ MSSM_OPT_DECODE_PATH = 5
 MSSM_OPT_TEST_HOOKS = 6
 MSSM_OPT_ROWS_PER_CTA = 7
 MSSM_OPT_ROWS_PER_THREAD = 8
-MSSM_OPT_GATED_WARPS, MSSM_OPT_GATED_SPLIT, MSSM_OPT_W4_WARPS, MSSM_OPT_GATED_STEP_ROWS = 9, 10, 11, 12
+MSSM_OPT_GATED_WARPS, MSSM_OPT_GATED_SPLIT, MSSM_OPT_W4_PLAN, MSSM_OPT_GATED_STEP_ROWS = 9, 10, 11, 12
 MSSM_DISC_EULER, MSSM_DISC_ZOH = 0, 1
 SCHEDULES = {"forward": 1, "summaries+forward": 2, "chained": 3, "fused": 4, "split": 5}
 DECODE_PATHS = {"stream": 1, "bulk_tile": 2, "per_row": 3}

@@ -41,7 +41,7 @@ int g_rows_per_thread = 0;  // 0 automatic, else 1 or 2
 int g_decode_path = 0;  // MSSM_OPT_DECODE_PATH
 int g_gated_warps = 0;  // MSSM_OPT_GATED_WARPS
 int g_gated_split = 0;  // MSSM_OPT_GATED_SPLIT
-int g_w4_warps = 0;     // MSSM_OPT_W4_WARPS
+int g_w4_plan = 0;     // MSSM_OPT_W4_PLAN
 int g_step_rows = 0;    // MSSM_OPT_GATED_STEP_ROWS
 int g_test_hooks = 0;   // MSSM_OPT_TEST_HOOKS  // -1 automatic, else the forced LaunchShape mode
 
@@ -397,10 +397,10 @@ mssm_status mssm_set_option(int option, int64_t value) {
         return fail(MSSM_ERR_INVALID_ARG, "GATED_STEP_ROWS takes 0, 1, 2 or 4");
       g_step_rows = int(value);
       return MSSM_OK;
-    case MSSM_OPT_W4_WARPS:
-      if (value != 0 && value != 4 && value != 8 && value != 16)
-        return fail(MSSM_ERR_INVALID_ARG, "W4_WARPS takes 0, 4, 8 or 16");
-      g_w4_warps = int(value);
+    case MSSM_OPT_W4_PLAN:
+      if (value != 0 && value != 2 && value != 8 && value != 16)
+        return fail(MSSM_ERR_INVALID_ARG, "W4_PLAN takes 0, 2, 8 or 16");
+      g_w4_plan = int(value);
       return MSSM_OK;
     case MSSM_OPT_KERNEL_TIMING:
       if (value != 0 && value != 1) return fail(MSSM_ERR_INVALID_ARG, "KERNEL_TIMING takes 0 or 1");
@@ -1458,7 +1458,7 @@ mssm_status mssm_gated_state_update(mssm_tensor* state, const mssm_tensor* x, co
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
   const int64_t per = vec ? Dd / 4 : Dd, want = int64_t(device_state(dev)->sm_count) * 512;
-  const int rows = g_step_rows ? g_step_rows : Bt >= 4 && per * Bt / 4 >= want ? 4 : Bt >= 2 && per * Bt / 2 >= want ? 2 : 1;
+  const int rows = g_step_rows ? g_step_rows : Bt >= 2 && per * Bt / 2 >= want ? 2 : 1;
   e = tracked(MSSM_KERNEL_GATED_STEP, s, [&] { return mssm::launch_gated_step(a, vec, rows, dt, s); });
   if (e != cudaSuccess) return cuda_fail(e, "gated state update launch");
   return MSSM_OK;
@@ -1574,15 +1574,25 @@ mssm_status mssm_w4_linear(const mssm_tensor* x, const mssm_tensor* qweight, con
   a.bias = bias ? static_cast<const float*>(bias->data) : nullptr; a.bias_s = bias ? bias->stride[0] : 0;
   a.out = out->data; a.o_sm = out->stride[0]; a.o_sn = out->stride[1];
   a.M = int(M); a.N = int(N); a.K = int(K);
-  a.blocks = int(w.blocks); a.groups = int(w.groups); a.group = int(group);
+  a.tiles = int(w.tiles); a.blocks = int(w.blocks); a.groups = int(w.groups); a.group = int(group);
   a.group_shift = -1;
   for (int k = 0; k < 26; ++k)
     if ((int64_t(32) << k) == group) a.group_shift = k;
   a.vec_x = aligned16(x->data) && (M == 1 || (x->stride[0] * int64_t(esize(dt))) % 16 == 0);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   std::lock_guard<std::mutex> lk(g_mu);
-  const int warps = g_w4_warps ? g_w4_warps : 8;
-  cudaError_t e = tracked(MSSM_KERNEL_W4_LINEAR, s, [&] { return mssm::launch_w4_linear(a, warps, dt, qscales->dtype, s); });
+  // Two tiles of 16 outputs a CTA share the loop's and x's instructions, where that leaves every SM half a CTA
+  // or more; few tiles of a long row take more warps instead.  Device us (with 6 to 8 of launch) for 2 tiles /
+  // 8 warps / 16 warps, bf16: 1x5120x20480 27 / 29 / 31, 32x5120x20480 53 / 80 / 86, 16x5120x2560 14 / 16 / 18,
+  // 4x16384x2048 31 / 23 / 18, 1x16384x1024 25 / 21 / 16.
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  const int64_t sms = device_state(dev)->sm_count;
+  int choice = w.tiles * ((M + 31) / 32) >= sms ? 2 : w.blocks >= 128 ? 16 : 8;
+  if (g_w4_plan) choice = g_w4_plan;
+  const mssm::W4Plan plan = choice == 2 ? mssm::W4Plan{2, 8} : mssm::W4Plan{1, choice};
+  e = tracked(MSSM_KERNEL_W4_LINEAR, s, [&] { return mssm::launch_w4_linear(a, plan, dt, qscales->dtype, s); });
   if (e != cudaSuccess) return cuda_fail(e, "4-bit linear launch");
   return MSSM_OK;
 }

@@ -52,7 +52,10 @@ cudaError_t launch_gated_bwd(const GatedArgs& a, int warps, int dtype, cudaStrea
 cudaError_t launch_gated_step(const GatedStepArgs& a, bool vec, int rows, int dtype, cudaStream_t s);
 // 4-bit linear map: the layout of a weight, and the product.
 cudaError_t launch_w4_pack(const W4PackArgs& a, int scale_dtype, cudaStream_t s);
-cudaError_t launch_w4_linear(const W4Args& a, int warps, int dtype, int scale_dtype, cudaStream_t s);
+struct W4Plan {
+  int tiles, warps;  // of a CTA: 2 tiles and 8 warps, or 1 tile and 8 or 16 warps
+};
+cudaError_t launch_w4_linear(const W4Args& a, W4Plan plan, int dtype, int scale_dtype, cudaStream_t s);
 // Reads (and optionally clears) the current device's error word.
 cudaError_t read_device_error(unsigned int* value, bool clear);
 

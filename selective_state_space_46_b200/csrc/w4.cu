@@ -3,10 +3,10 @@
 
 namespace mssm {
 
-template <typename T, typename S, int NT, int W, bool HALF, bool ZERO>
+template <typename T, typename S, int NT, int TT, int W, bool HALF, bool ZERO>
 static cudaError_t w4_run(const W4Args& a, cudaStream_t s) {
-  constexpr size_t smem = w4_smem<T, S, NT, W, HALF, ZERO>();
-  const auto kernel = w4_linear_kernel<T, S, NT, W, HALF, ZERO>;
+  constexpr size_t smem = w4_smem<T, S, NT, TT, W, HALF, ZERO>();
+  const auto kernel = w4_linear_kernel<T, S, NT, TT, W, HALF, ZERO>;
   if (smem > 48 * 1024) {  // once for every device; the caller holds the library's lock
     static uint64_t allowed = 0;
     int dev = -1;
@@ -17,33 +17,35 @@ static cudaError_t w4_run(const W4Args& a, cudaStream_t s) {
     }
     if (e != cudaSuccess) return e;
   }
-  const dim3 g(unsigned((a.N + kW4Rows - 1) / kW4Rows), unsigned((a.M + 8 * NT - 1) / (8 * NT)));
+  const dim3 g(unsigned((a.tiles + TT - 1) / TT), unsigned((a.M + 8 * NT - 1) / (8 * NT)));
   kernel<<<g, 32 * W, smem, s>>>(a);
   return cudaGetLastError();
 }
 
-template <typename T, typename S, int NT, int W>
+template <typename T, typename S, int NT, int TT, int W>
 static cudaError_t w4_w(const W4Args& a, cudaStream_t s) {
-  if (a.group % kW4K != 0) return a.zero ? w4_run<T, S, NT, W, true, true>(a, s) : w4_run<T, S, NT, W, true, false>(a, s);
-  return a.zero ? w4_run<T, S, NT, W, false, true>(a, s) : w4_run<T, S, NT, W, false, false>(a, s);
+  if (a.group % kW4K != 0)
+    return a.zero ? w4_run<T, S, NT, TT, W, true, true>(a, s) : w4_run<T, S, NT, TT, W, true, false>(a, s);
+  return a.zero ? w4_run<T, S, NT, TT, W, false, true>(a, s) : w4_run<T, S, NT, TT, W, false, false>(a, s);
 }
 
 template <typename T, typename S, int NT>
-static cudaError_t w4_n(const W4Args& a, int warps, cudaStream_t s) {
-  return warps == 4 ? w4_w<T, S, NT, 4>(a, s) : warps == 8 ? w4_w<T, S, NT, 8>(a, s) : w4_w<T, S, NT, 16>(a, s);
+static cudaError_t w4_n(const W4Args& a, W4Plan plan, cudaStream_t s) {
+  if (plan.tiles == 2) return w4_w<T, S, NT, 2, 8>(a, s);
+  return plan.warps == 8 ? w4_w<T, S, NT, 1, 8>(a, s) : w4_w<T, S, NT, 1, 16>(a, s);
 }
 
 template <typename T, typename S>
-static cudaError_t w4_s(const W4Args& a, int warps, cudaStream_t s) {
-  if (a.M <= 8) return w4_n<T, S, 1>(a, warps, s);
+static cudaError_t w4_s(const W4Args& a, W4Plan plan, cudaStream_t s) {
+  if (a.M <= 8) return w4_n<T, S, 1>(a, plan, s);
   if constexpr (sizeof(T) == 2)
-    if (a.M > 16) return w4_n<T, S, 4>(a, warps, s);
-  return w4_n<T, S, 2>(a, warps, s);  // fp32: the ring of 32 tokens' x would not fit
+    if (a.M > 16) return w4_n<T, S, 4>(a, plan, s);
+  return w4_n<T, S, 2>(a, plan, s);  // fp32: the ring of 32 tokens' x would not fit
 }
 
-cudaError_t launch_w4_linear(const W4Args& a, int warps, int dtype, int scale_dtype, cudaStream_t s) {
-  if (dtype == 1) return scale_dtype == 1 ? w4_s<uint16_t, uint16_t>(a, warps, s) : w4_s<uint16_t, float>(a, warps, s);
-  return scale_dtype == 1 ? w4_s<float, uint16_t>(a, warps, s) : w4_s<float, float>(a, warps, s);
+cudaError_t launch_w4_linear(const W4Args& a, W4Plan plan, int dtype, int scale_dtype, cudaStream_t s) {
+  if (dtype == 1) return scale_dtype == 1 ? w4_s<uint16_t, uint16_t>(a, plan, s) : w4_s<uint16_t, float>(a, plan, s);
+  return scale_dtype == 1 ? w4_s<float, uint16_t>(a, plan, s) : w4_s<float, float>(a, plan, s);
 }
 
 cudaError_t launch_w4_pack(const W4PackArgs& a, int scale_dtype, cudaStream_t s) {

@@ -32,7 +32,7 @@ struct W4Args {
   void* out;                   // [M, N]
   int64_t o_sm, o_sn;
   int M, N, K;
-  int blocks, groups, group;   // blocks of 64 inputs; groups stored per tile; inputs per group
+  int tiles, blocks, groups, group;   // tiles of 16 outputs; blocks of 64 inputs; groups stored per tile; inputs per group
   int group_shift;             // log2(group / 32), or -1 when the group is no power of two
   bool vec_x;                  // rows of x start on 16-byte boundaries
 };
@@ -155,181 +155,204 @@ __device__ __forceinline__ float2 scale_pair(const uint16_t* s) {
   return make_float2(bf16lo(u), bf16hi(u));
 }
 
-template <int BYTES>
-__device__ __forceinline__ void copy_async(unsigned to, const void* from) {
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(BYTES) : "memory");
-}
-
-// Asks for 8 inputs of a token from k on (zeros behind the last one).  Rows off a 16-byte boundary: fp32 by the
-// element, bf16 through registers.
+// Asks for 8 inputs of a token, from k on.  inner: all of them exist and start on a 16-byte boundary; otherwise
+// zeros stand behind the last one, fp32 comes by the element and bf16 through registers.
 template <typename T>
-__device__ __forceinline__ void x_ask(char* to, const T* x, int k, int K, bool vec) {
-  constexpr int kPiece = 16 / int(sizeof(T));
-  const unsigned at = unsigned(__cvta_generic_to_shared(to));
+__device__ __forceinline__ void x_ask(unsigned to, const T* x, int k, int K, bool inner) {
+  if (inner) {
 #pragma unroll
-  for (int v = 0; v < 8 / kPiece; ++v) {
-    const int k0 = k + v * kPiece, n = max(min(K - k0, kPiece), 0);
-    if (vec) {
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(at + v * 512), "l"(x + (n ? k0 : 0)),
-                   "r"(n * int(sizeof(T)))
+    for (int v = 0; v < int(sizeof(T)) / 2; ++v)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(to + v * 512), "l"(x + v * (16 / sizeof(T))) : "memory");
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const bool in = k + j < K;
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + j / 4 * 512 + 4 * (j % 4)), "l"(x - k + (in ? k + j : 0)),
+                   "r"(in ? 4 : 0)
                    : "memory");
-    } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-      for (int j = 0; j < kPiece; ++j)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(at + v * 512 + 4 * j), "l"(x + (j < n ? k0 + j : 0)),
-                     "r"(j < n ? 4 : 0)
-                     : "memory");
-    } else {
-      uint32_t u[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        u[j] = (2 * j < n ? uint32_t(x[k0 + 2 * j]) : 0u) | (2 * j + 1 < n ? uint32_t(x[k0 + 2 * j + 1]) << 16 : 0u);
-      *reinterpret_cast<uint4*>(to) = make_uint4(u[0], u[1], u[2], u[3]);
     }
+  } else {
+    uint32_t u[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      u[j] = (k + 2 * j < K ? uint32_t(x[2 * j]) : 0u) | (k + 2 * j + 1 < K ? uint32_t(x[2 * j + 1]) << 16 : 0u);
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]) : "memory");
   }
 }
 
-// One CTA per 16 outputs and 8 * NT tokens; its W warps take every W-th block of 64 inputs and add up in shared
-// memory, in order.  HALF: the group is an odd multiple of 32, so both halves of a block have their own
-// scale.  The stream of weights is what bounds a few tokens: every lane has its 16 bytes of the next blocks,
-// their scales and its x on the way into its own places of shared memory (no other lane reads them, so the
-// copies' own order is all the synchronisation).
-
-template <typename T, typename S, int NT, bool HALF, bool ZERO>
+// One CTA per TT tiles of 16 outputs and 8 * NT tokens; its W warps take every W-th block of 64 inputs and add up
+// in shared memory, in order.  HALF: the group is an odd multiple of 32, so both halves of a block have
+// their own scale.  Every lane has its 16 bytes of the next blocks, their scales and its x on the way into its
+// own places of shared memory (no other lane reads them, so the copies' own order is all the
+// synchronisation).  One token is bound by the instructions that unpack the codes as much as by the stream
+// of weights: 60 a block of 1024 codes, beside those of the loop and of x, which two tiles share.
+template <typename T, typename S, int NT, int TT, bool HALF, bool ZERO>
 struct W4Ring {
   static constexpr int kSets = HALF ? 2 : 1;
   static constexpr int kPair = 2 * int(sizeof(S));
   static constexpr int kXPart = 32 * 8 * int(sizeof(T));  // of half a block and 8 tokens
-  static constexpr int kX = 512, kScale = kX + 2 * NT * kXPart, kZero = kScale + 32 * kPair * kSets;  // places in a slot
-  static constexpr int kSlot = kZero + (ZERO ? 32 * 4 * kSets : 0);
+  // places in a slot: weights, x, scales, zero points
+  static constexpr int kX = 512 * TT, kScale = kX + 2 * NT * kXPart, kZero = kScale + 32 * kPair * kSets * TT;
+  static constexpr int kSlot = kZero + (ZERO ? 32 * 4 * kSets * TT : 0);
   // about 7 KB of a warp, so that 32 warps of an SM have 48 KB of weights on the way
   static constexpr int kSlots = 7168 / kSlot > 6 ? 6 : 7168 / kSlot < 2 ? 2 : 7168 / kSlot;
   static constexpr int kWarp = kSlot * kSlots;
 };
 
-template <typename T, typename S, int NT, int W, bool HALF, bool ZERO>
+template <typename T, typename S, int NT, int TT, int W, bool HALF, bool ZERO>
 __global__ void __launch_bounds__(32 * W) w4_linear_kernel(const W4Args p) {
-  using Ring = W4Ring<T, S, NT, HALF, ZERO>;
-  constexpr int kSlots = Ring::kSlots;
+  using Ring = W4Ring<T, S, NT, TT, HALF, ZERO>;
+  constexpr int kSlots = Ring::kSlots, kSets = Ring::kSets;
   extern __shared__ __align__(16) char s_mem[];  // the warps' rings, then their sums
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, c = lane % 4;
-  const int tile = blockIdx.x, m0 = blockIdx.y * (8 * NT);
-  const uint4* q = p.q + int64_t(tile) * p.blocks * 32 + lane;
-  const S* scale = static_cast<const S*>(p.scale) + (int64_t(tile) * p.groups * 8 + g) * 2;
-  const uint8_t* zero = ZERO ? p.zero + (int64_t(tile) * p.groups * 8 + (g & ~1)) * 2 : nullptr;  // 4 bytes: g and g ^ 1
-  char* ring = s_mem + warp * Ring::kWarp;
-  const unsigned ring_at = unsigned(__cvta_generic_to_shared(ring));
+  const int tile0 = blockIdx.x * TT, m0 = blockIdx.y * (8 * NT);
+  // a last CTA without a second tile computes its first one twice
+  const int64_t next_q = TT > 1 && tile0 + 1 < p.tiles ? int64_t(p.blocks) * 32 : 0;
+  const int64_t next_s = TT > 1 && tile0 + 1 < p.tiles ? int64_t(p.groups) * 16 : 0;
+  const uint4* q = p.q + (int64_t(tile0) * p.blocks + warp) * 32 + lane;
+  const S* scale = static_cast<const S*>(p.scale) + (int64_t(tile0) * p.groups * 8 + g) * 2;
+  const uint8_t* zero = ZERO ? p.zero + (int64_t(tile0) * p.groups * 8 + (g & ~1)) * 2 : nullptr;  // 4 bytes: g and g ^ 1
   const T* xr[NT];
   bool on[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int m = m0 + 8 * n + g;
     on[n] = m < p.M;
-    xr[n] = static_cast<const T*>(p.x) + (on[n] ? m : 0) * p.x_sm;
+    xr[n] = static_cast<const T*>(p.x) + (on[n] ? m : 0) * p.x_sm + warp * kW4K + 8 * c;
   }
-  auto ask = [&](int slot, int kb) {
-    if (kb < p.blocks) {
-      const unsigned to = ring_at + slot * Ring::kSlot;
-      copy_async<16>(to + lane * 16, q + int64_t(kb) * 32);
+  const unsigned ring = unsigned(__cvta_generic_to_shared(s_mem)) + warp * Ring::kWarp, ring_end = ring + Ring::kWarp;
+  // the pointers are those of the block that is asked for next
+  int asked = warp;
+  unsigned to = ring;
+  auto ask = [&] {
+    if (asked < p.blocks) {
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + t * 512 + lane * 16), "l"(q + t * next_q) : "memory");
+      const int k = asked * kW4K + 8 * c;
+      const bool inner = p.vec_x && (asked + 1) * kW4K <= p.K;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
         if (on[n])
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            x_ask(ring + slot * Ring::kSlot + Ring::kX + (2 * n + h) * Ring::kXPart + lane * 16, xr[n],
-                  kb * kW4K + 32 * h + 8 * c, p.K, p.vec_x);
+            x_ask(to + Ring::kX + (2 * n + h) * Ring::kXPart + lane * 16, xr[n] + 32 * h, k + 32 * h, p.K, inner);
 #pragma unroll
-      for (int h = 0; h < Ring::kSets; ++h) {
-        const unsigned u = unsigned(2 * kb + h);  // in units of 32 inputs
+      for (int h = 0; h < kSets; ++h) {
+        const unsigned u = unsigned(2 * asked + h);  // in units of 32 inputs
         const unsigned grp = p.group_shift >= 0 ? u >> p.group_shift : u / unsigned(p.group / 32);
-        copy_async<Ring::kPair>(to + Ring::kScale + (32 * h + lane) * Ring::kPair, scale + size_t(grp) * 16);
-        if (ZERO) copy_async<4>(to + Ring::kZero + (32 * h + lane) * 4, zero + size_t(grp) * 16);
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to + Ring::kScale + (32 * (kSets * t + h) + lane) * Ring::kPair),
+                       "l"(scale + size_t(grp) * 16 + t * next_s), "n"(Ring::kPair)
+                       : "memory");
+          if (ZERO)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + Ring::kZero + (32 * (kSets * t + h) + lane) * 4),
+                         "l"(zero + size_t(grp) * 16 + t * next_s)
+                         : "memory");
+        }
       }
+      q += 32 * W;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) xr[n] += W * kW4K;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
+    asked += W;
+    to += Ring::kSlot;
+    if (to == ring_end) to = ring;
   };
 #pragma unroll
-  for (int j = 0; j < kSlots - 1; ++j) ask(j, warp + j * W);
+  for (int j = 0; j < kSlots - 1; ++j) ask();
 
-  float acc[NT][4];
+  float acc[TT][NT][4];
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) acc[n][k] = 0.0f;
-
-  int slot = 0;
+  for (int e = 0; e < TT * NT * 4; ++e) (&acc[0][0][0])[e] = 0.0f;
+  const char* at = s_mem + warp * Ring::kWarp;
   for (int kb = warp; kb < p.blocks; kb += W) {
-    ask(slot == 0 ? kSlots - 1 : slot - 1, kb + (kSlots - 1) * W);
+    ask();
     asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 1) : "memory");
-    const char* at = ring + slot * Ring::kSlot;
-    const uint4 w = *reinterpret_cast<const uint4*>(at + lane * 16);
-    const uint32_t wlo[2] = {w.x, w.y}, whi[2] = {w.z, w.w};
-    float part[NT][4];
-    uint32_t z0 = 0x43084308u, z1 = 0x43084308u;
+    uint32_t wlo[TT][2], whi[TT][2];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      const uint4 w = *reinterpret_cast<const uint4*>(at + t * 512 + lane * 16);
+      wlo[t][0] = w.x; wlo[t][1] = w.y; whi[t][0] = w.z; whi[t][1] = w.w;
+    }
+    float part[TT][NT][4];
+    uint32_t z0[TT], z1[TT];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int set = HALF ? h : 0;
       if (h == 0 || HALF) {
-        if (ZERO) {
-          const uint32_t zz = *reinterpret_cast<const uint32_t*>(at + Ring::kZero + (32 * set + lane) * 4) >> (16 * (g & 1));
-          z0 = (zz & 0xffu) * 0x10001u | 0x43004300u;
-          z1 = (zz >> 8 & 0xffu) * 0x10001u | 0x43004300u;
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          z0[t] = z1[t] = 0x43084308u;
+          if (ZERO) {
+            const uint32_t zz = *reinterpret_cast<const uint32_t*>(at + Ring::kZero + (32 * (kSets * t + set) + lane) * 4) >> (16 * (g & 1));
+            z0[t] = (zz & 0xffu) * 0x10001u | 0x43004300u;
+            z1[t] = (zz >> 8 & 0xffu) * 0x10001u | 0x43004300u;
+          }
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) part[n][k] = 0.0f;
+        for (int e = 0; e < TT * NT * 4; ++e) (&part[0][0][0])[e] = 0.0f;
       }
-      uint32_t a[2][4];
+      uint32_t a[TT][2][4];
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        a[s][0] = w4_pair(wlo[h], 2 * s, z0);
-        a[s][1] = w4_pair(whi[h], 2 * s, z1);
-        a[s][2] = w4_pair(wlo[h], 2 * s + 1, z0);
-        a[s][3] = w4_pair(whi[h], 2 * s + 1, z1);
-      }
+      for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          a[t][s][0] = w4_pair(wlo[t][h], 2 * s, z0[t]);
+          a[t][s][1] = w4_pair(whi[t][h], 2 * s, z1[t]);
+          a[t][s][2] = w4_pair(wlo[t][h], 2 * s + 1, z0[t]);
+          a[t][s][3] = w4_pair(whi[t][h], 2 * s + 1, z1[t]);
+        }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         XFrag<T> xf{};
         if (on[n]) xf = x_frag<T>(at + Ring::kX + (2 * n + h) * Ring::kXPart + lane * 16);
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+        for (int t = 0; t < TT; ++t)
 #pragma unroll
-          for (int t = 0; t < XFrag<T>::kParts; ++t) mma_bf16(part[n], a[s], xf.v[t][2 * s], xf.v[t][2 * s + 1]);
+          for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int e = 0; e < XFrag<T>::kParts; ++e) mma_bf16(part[t][n], a[t][s], xf.v[e][2 * s], xf.v[e][2 * s + 1]);
       }
       if (h == 1 || HALF) {
-        const float2 sc = scale_pair(reinterpret_cast<const S*>(at + Ring::kScale + (32 * set + lane) * Ring::kPair));
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          acc[n][0] = fmaf(sc.x, part[n][0], acc[n][0]);
-          acc[n][1] = fmaf(sc.x, part[n][1], acc[n][1]);
-          acc[n][2] = fmaf(sc.y, part[n][2], acc[n][2]);
-          acc[n][3] = fmaf(sc.y, part[n][3], acc[n][3]);
+        for (int t = 0; t < TT; ++t) {
+          const float2 sc = scale_pair(reinterpret_cast<const S*>(at + Ring::kScale + (32 * (kSets * t + set) + lane) * Ring::kPair));
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            acc[t][n][0] = fmaf(sc.x, part[t][n][0], acc[t][n][0]);
+            acc[t][n][1] = fmaf(sc.x, part[t][n][1], acc[t][n][1]);
+            acc[t][n][2] = fmaf(sc.y, part[t][n][2], acc[t][n][2]);
+            acc[t][n][3] = fmaf(sc.y, part[t][n][3], acc[t][n][3]);
+          }
         }
       }
     }
-    slot = slot + 1 == kSlots ? 0 : slot + 1;
+    at += Ring::kSlot;
+    if (at == s_mem + (warp + 1) * Ring::kWarp) at -= Ring::kWarp;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();
   // accumulator element: rows g (0, 1) and g + 8 (2, 3), tokens 2c and 2c + 1
-  float* s_acc = reinterpret_cast<float*>(s_mem);  // [W][8 NT][kW4Rows + 1]
+  float* s_acc = reinterpret_cast<float*>(s_mem);  // [W][8 NT][16 TT + 1]
+  constexpr int kRow = kW4Rows * TT + 1;
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+  for (int t = 0; t < TT; ++t)
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      s_acc[(warp * 8 * NT + 8 * n + 2 * c + (k & 1)) * (kW4Rows + 1) + g + 8 * (k >> 1)] = acc[n][k];
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        s_acc[(warp * 8 * NT + 8 * n + 2 * c + (k & 1)) * kRow + kW4Rows * t + g + 8 * (k >> 1)] = acc[t][n][k];
   __syncthreads();
-  for (int e = threadIdx.x; e < 8 * NT * kW4Rows; e += 32 * W) {
-    const int m = e / kW4Rows, r = e % kW4Rows;
-    const int n = tile * kW4Rows + r;
+  for (int e = threadIdx.x; e < 8 * NT * kW4Rows * TT; e += 32 * W) {
+    const int m = e / (kW4Rows * TT), r = e % (kW4Rows * TT);
+    const int64_t n = int64_t(tile0) * kW4Rows + r;
     if (m0 + m >= p.M || n >= p.N) continue;
     float v = 0.0f;
 #pragma unroll
-    for (int k = 0; k < W; ++k) v += s_acc[(k * 8 * NT + m) * (kW4Rows + 1) + r];
+    for (int k = 0; k < W; ++k) v += s_acc[(k * 8 * NT + m) * kRow + r];
     if (p.bias) v += p.bias[n * p.bias_s];
     T* o = static_cast<T*>(p.out) + (m0 + m) * p.o_sm + n * p.o_sn;
     if constexpr (sizeof(T) == 2) *o = f_to_bf16(v);
@@ -338,9 +361,10 @@ __global__ void __launch_bounds__(32 * W) w4_linear_kernel(const W4Args p) {
 }
 
 // shared memory of a CTA
-template <typename T, typename S, int NT, int W, bool HALF, bool ZERO>
+template <typename T, typename S, int NT, int TT, int W, bool HALF, bool ZERO>
 constexpr size_t w4_smem() {
-  const size_t ring = size_t(W) * W4Ring<T, S, NT, HALF, ZERO>::kWarp, sums = size_t(W) * 8 * NT * (kW4Rows + 1) * 4;
+  const size_t ring = size_t(W) * W4Ring<T, S, NT, TT, HALF, ZERO>::kWarp,
+               sums = size_t(W) * 8 * NT * (kW4Rows * TT + 1) * 4;
   return ring > sums ? ring : sums;
 }
 
