@@ -338,6 +338,8 @@ class mssm_gated_ext(ctypes.Structure):
 
 assert ctypes.sizeof(mssm_tensor) == 80 and ctypes.sizeof(mssm_gated_ext) == _Block.EXT.size
 _block = _Block()
+_STEP = ctypes.cast(_lib.mssm_gated_state_update, ctypes.c_void_p).value
+_LINEAR = ctypes.cast(_lib.mssm_w4_linear, ctypes.c_void_p).value
 
 
 def _call(stream, device, fn, *args):
@@ -514,6 +516,11 @@ def gated_state_update(state, x, r, i, lam, r_bias=None, i_bias=None, z=None, c=
                        stream=None) -> torch.Tensor:
     """One decode step of the gated recurrence on ``x`` [Bt, D] (``state`` [Bt, D] updated in place);
     returns ``out``."""
+    if stream is None:
+        out = _marshal.step(_STEP, state, x, r, i, lam, r_bias, i_bias, z, c, out)
+        if type(out) is int:
+            _check(out)
+        return out
     if out is None:
         with _allocating_on(stream, x.device):
             out = torch.empty_like(x, memory_format=torch.contiguous_format)
@@ -552,10 +559,16 @@ def w4_linear(x, weight: W4Weight, bias=None, out=None, stream=None) -> torch.Te
     """``x`` [M, K] times the packed weight's transpose, plus ``bias`` [N]; returns ``out`` [M, N]."""
     if x.dim() != 2 or x.shape[1] != weight.in_features:
         raise ValueError(f"x: expected [M, {weight.in_features}], got {list(x.shape)}")
+    if out is not None and out.shape != (x.shape[0], weight.out_features):
+        raise ValueError(f"out: expected [{x.shape[0]}, {weight.out_features}], got {list(out.shape)}")
+    if stream is None:
+        out = _marshal.linear(_LINEAR, x, weight.qweight, weight.qscales, weight.qzeros, weight.group_size, bias,
+                              weight.out_features, out)
+        if type(out) is int:
+            _check(out)
+        return out
     if out is None:
         with _allocating_on(stream, x.device):
             out = torch.empty(x.shape[0], weight.out_features, device=x.device, dtype=x.dtype)
-    elif out.shape != (x.shape[0], weight.out_features):
-        raise ValueError(f"out: expected [{x.shape[0]}, {weight.out_features}], got {list(out.shape)}")
     mssm_w4_linear(x, weight.qweight, weight.qscales, weight.qzeros, weight.group_size, bias, out, stream)
     return out

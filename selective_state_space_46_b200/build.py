@@ -59,9 +59,10 @@ def build_marshal(force: bool = False, verbose: bool = False) -> str:
         return MARSHAL
     tmp = MARSHAL + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", f"-I{INCLUDE}", f"-I{base}/include",
-           f"-I{base}/include/torch/csrc/api/include", f"-I{sysconfig.get_paths()['include']}",
+           f"-I{base}/include/torch/csrc/api/include", f"-I{os.path.dirname(os.path.dirname(_nvcc()))}/include",
+           f"-I{sysconfig.get_paths()['include']}",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", MARSHAL_SRC, "-o", tmp,
-           f"-L{base}/lib", "-ltorch_python", "-ltorch_cpu", "-lc10"]
+           f"-L{base}/lib", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -1,7 +1,12 @@
-// Writes a call's tensor descriptors for the Python binding.  A decode step is a few microseconds on the GPU;
-// reading eight tensors' pointers, shapes and strides from Python takes longer than that.
+// The Python binding's fast part: writes a call's tensor descriptors, and makes the decode path's two calls.
+// A decode step is a few microseconds on the GPU; reading eight tensors' pointers, shapes and strides from
+// Python takes longer than that.
 #include <Python.h>
 
+#include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "mssm.h"
@@ -18,9 +23,41 @@ int dtype_of(const at::Tensor& t) {
   }
 }
 
+// Fills `d` for a tensor and sets `device` or compares with it.  False: a Python error is set.
+bool fill(PyObject* arg, mssm_tensor& d, int& device) {
+  if (!THPVariable_Check(arg)) {
+    PyErr_Format(PyExc_TypeError, "expected a tensor, got %.100s", Py_TYPE(arg)->tp_name);
+    return false;
+  }
+  const at::Tensor& t = THPVariable_Unpack(arg);
+  if (!t.is_cuda()) {
+    PyErr_SetString(PyExc_ValueError, "this operator runs on CUDA tensors only");
+    return false;
+  }
+  if (t.layout() != at::kStrided || t.dim() < 1 || t.dim() > 4) {
+    PyErr_SetString(PyExc_ValueError, "expected strided tensors of 1 to 4 dims");
+    return false;
+  }
+  const int on = t.get_device();
+  if (device >= 0 && on != device) {
+    PyErr_Format(PyExc_ValueError, "all tensors must be on cuda:%d (got one on cuda:%d)", device, on);
+    return false;
+  }
+  device = on;
+  d = mssm_tensor{};
+  d.data = t.numel() > 0 ? t.data_ptr() : nullptr;
+  d.dtype = dtype_of(t);
+  d.ndim = int32_t(t.dim());
+  for (int k = 0; k < int(t.dim()); ++k) {
+    d.shape[k] = t.size(k);
+    d.stride[k] = t.stride(k);
+  }
+  return true;
+}
+
 // describe(block, *tensors) -> (device index, addresses): the descriptor of tensor j goes to block[j], and None
 // stays None.  All tensors have to be on one CUDA device.
-PyObject* describe(PyObject*, PyObject* const* args, Py_ssize_t n) {
+PyObject* describe(PyObject* const* args, Py_ssize_t n) {
   if (n < 2) {
     PyErr_SetString(PyExc_TypeError, "describe(block, *tensors)");
     return nullptr;
@@ -34,45 +71,22 @@ PyObject* describe(PyObject*, PyObject* const* args, Py_ssize_t n) {
   PyObject* out = PyTuple_New(n);
   if (!out) return nullptr;
   for (Py_ssize_t j = 1; j < n; ++j) {
+    PyObject* item = nullptr;
     if (args[j] == Py_None) {
       Py_INCREF(Py_None);
-      PyTuple_SET_ITEM(out, j, Py_None);
-      continue;
+      item = Py_None;
+    } else if (fill(args[j], block[j - 1], device)) {
+      item = PyLong_FromVoidPtr(&block[j - 1]);
     }
-    if (!THPVariable_Check(args[j])) {
-      PyErr_Format(PyExc_TypeError, "expected a tensor or None, got %.100s", Py_TYPE(args[j])->tp_name);
-      break;
+    if (!item) {
+      Py_DECREF(out);
+      return nullptr;
     }
-    const at::Tensor& t = THPVariable_Unpack(args[j]);
-    if (!t.is_cuda()) {
-      PyErr_SetString(PyExc_ValueError, "this operator runs on CUDA tensors only");
-      break;
-    }
-    if (t.layout() != at::kStrided || t.dim() < 1 || t.dim() > 4) {
-      PyErr_SetString(PyExc_ValueError, "expected strided tensors of 1 to 4 dims");
-      break;
-    }
-    const int on = t.get_device();
-    if (device >= 0 && on != device) {
-      PyErr_Format(PyExc_ValueError, "all tensors must be on cuda:%d (got one on cuda:%d)", device, on);
-      break;
-    }
-    device = on;
-    mssm_tensor& d = block[j - 1];
-    d = mssm_tensor{};
-    d.data = t.numel() > 0 ? t.data_ptr() : nullptr;
-    d.dtype = dtype_of(t);
-    d.ndim = int32_t(t.dim());
-    for (int k = 0; k < int(t.dim()); ++k) {
-      d.shape[k] = t.size(k);
-      d.stride[k] = t.stride(k);
-    }
-    PyObject* at = PyLong_FromVoidPtr(&d);
-    if (!at) break;
-    PyTuple_SET_ITEM(out, j, at);
+    PyTuple_SET_ITEM(out, j, item);
   }
-  if (!PyErr_Occurred() && device < 0) PyErr_SetString(PyExc_ValueError, "no tensor given");
-  PyObject* index = PyErr_Occurred() ? nullptr : PyLong_FromLong(device);
+  PyObject* index = nullptr;
+  if (device < 0) PyErr_SetString(PyExc_ValueError, "no tensor given");
+  else index = PyLong_FromLong(device);
   if (!index) {
     Py_DECREF(out);
     return nullptr;
@@ -81,21 +95,117 @@ PyObject* describe(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return out;
 }
 
-// C++ exceptions (a tensor without storage) become Python ones
-PyObject* describe_noexcept(PyObject* self, PyObject* const* args, Py_ssize_t n) {
-  try {
-    return describe(self, args, n);
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
-  } catch (...) {
-    PyErr_SetString(PyExc_RuntimeError, "unknown error while reading a tensor");
+// Descriptors of a call's tensors, and the call itself on the device's current stream.
+struct Call {
+  mssm_tensor d[9];
+  int device = -1;
+  int used = 0;
+  // null for None; `ok` turns false with a Python error
+  bool ok = true;
+  const mssm_tensor* in(PyObject* arg) {
+    if (!ok || arg == Py_None) return nullptr;
+    ok = fill(arg, d[used], device);
+    return ok ? &d[used++] : nullptr;
   }
-  return nullptr;
+  // the output given, or (new reference in `made`) a new one
+  template <typename F>
+  mssm_tensor* out(PyObject* arg, PyObject*& made, F make) {
+    if (!ok) return nullptr;
+    if (arg == Py_None) {
+      made = THPVariable_Wrap(make());
+      if (!made) ok = false;
+    } else {
+      Py_INCREF(arg);
+      made = arg;
+    }
+    return const_cast<mssm_tensor*>(ok ? in(made) : nullptr);
+  }
+  template <typename F>
+  PyObject* run(PyObject* made, F f) {
+    if (!ok) {
+      Py_XDECREF(made);
+      return nullptr;
+    }
+    c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(device));
+    void* stream = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream();
+    mssm_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = f(stream);
+    Py_END_ALLOW_THREADS
+    if (st == MSSM_OK) return made;
+    Py_DECREF(made);
+    return PyLong_FromLong(long(st));
+  }
+};
+
+// step(function, state, x, r, i, lam, r_bias, i_bias, z, decay scale, out) -> out, or the status of a failed call
+PyObject* step(PyObject* const* args, Py_ssize_t n) {
+  if (n != 11) {
+    PyErr_SetString(PyExc_TypeError, "step takes 11 arguments");
+    return nullptr;
+  }
+  const auto fn = reinterpret_cast<decltype(&mssm_gated_state_update)>(PyLong_AsVoidPtr(args[0]));
+  const double c = PyFloat_AsDouble(args[9]);
+  if (!fn || PyErr_Occurred()) return nullptr;
+  Call call;
+  auto* state = const_cast<mssm_tensor*>(call.in(args[1]));
+  const mssm_tensor *x = call.in(args[2]), *r = call.in(args[3]), *i = call.in(args[4]), *lam = call.in(args[5]),
+                    *rb = call.in(args[6]), *ib = call.in(args[7]), *z = call.in(args[8]);
+  PyObject* made = nullptr;
+  if (call.ok && !x) {
+    PyErr_SetString(PyExc_TypeError, "x: expected a tensor");
+    return nullptr;
+  }
+  mssm_tensor* out = call.out(args[10], made, [&] {
+    const at::Tensor& t = THPVariable_Unpack(args[2]);
+    return at::empty(t.sizes(), t.options().requires_grad(false));
+  });
+  return call.run(made, [&](void* s) { return fn(state, x, r, i, lam, rb, ib, z, float(c), out, s); });
+}
+
+// linear(function, x, qweight, qscales, qzeros, group, bias, outputs, out) -> out, or the status of a failed call
+PyObject* linear(PyObject* const* args, Py_ssize_t n) {
+  if (n != 9) {
+    PyErr_SetString(PyExc_TypeError, "linear takes 9 arguments");
+    return nullptr;
+  }
+  const auto fn = reinterpret_cast<decltype(&mssm_w4_linear)>(PyLong_AsVoidPtr(args[0]));
+  const int64_t group = PyLong_AsLongLong(args[5]), outputs = PyLong_AsLongLong(args[7]);
+  if (!fn || PyErr_Occurred()) return nullptr;
+  Call call;
+  const mssm_tensor *x = call.in(args[1]), *q = call.in(args[2]), *s = call.in(args[3]), *z = call.in(args[4]),
+                    *b = call.in(args[6]);
+  PyObject* made = nullptr;
+  if (call.ok && !x) {
+    PyErr_SetString(PyExc_TypeError, "x: expected a tensor");
+    return nullptr;
+  }
+  mssm_tensor* out = call.out(args[8], made, [&] {
+    const at::Tensor& t = THPVariable_Unpack(args[1]);
+    return at::empty({t.size(0), outputs}, t.options().requires_grad(false));
+  });
+  return call.run(made, [&](void* stream) { return fn(x, q, s, z, group, b, out, stream); });
+}
+
+// C++ exceptions (out of memory, a tensor without storage) become the Python ones that torch raises
+template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
+PyObject* guarded(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  return F(args, n);
+  END_HANDLE_TH_ERRORS
+}
+
+template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
+PyCFunction method() {
+  return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(guarded<F>));
 }
 
 PyMethodDef methods[] = {
-    {"describe", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(describe_noexcept)), METH_FASTCALL,
-     "describe(block, *tensors) -> (device index, *addresses of the tensors' descriptors)"},
+    {"describe", method<describe>(), METH_FASTCALL, "describe(block, *tensors) -> (device index, *descriptor addresses)"},
+    {"step", method<step>(), METH_FASTCALL,
+     "step(function, state, x, r, i, lam, r_bias, i_bias, z, decay_scale, out) -> out, or a failed call's status"},
+    {"linear", method<linear>(), METH_FASTCALL,
+     "linear(function, x, qweight, qscales, qzeros, group, bias, outputs, out) -> out, or a failed call's status"},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
