@@ -338,6 +338,9 @@ class mssm_gated_ext(ctypes.Structure):
 
 assert ctypes.sizeof(mssm_tensor) == 80 and ctypes.sizeof(mssm_gated_ext) == _Block.EXT.size
 _block = _Block()
+_SCAN = ctypes.cast(_lib.mssm_gated_scan_fwd, ctypes.c_void_p).value
+_SCAN_BWD = ctypes.cast(_lib.mssm_gated_scan_bwd, ctypes.c_void_p).value
+_GRADS = ("dx", "dr", "di", "dz", "dlam", "dr_bias", "di_bias", "dh0")
 _STEP = ctypes.cast(_lib.mssm_gated_state_update, ctypes.c_void_p).value
 _LINEAR = ctypes.cast(_lib.mssm_w4_linear, ctypes.c_void_p).value
 
@@ -479,6 +482,11 @@ def gated_scan_fwd(x, r, i, lam, r_bias=None, i_bias=None, z=None, c=8.0, h0=Non
     ``i`` (both before bias and sigmoid), decay rate ``c * softplus(lam)`` and optional silu gate ``z``,
     from ``h0`` [S, D] when given, over packed sequences when ``cu_seqlens`` is.  Returns ``(out,
     last_state)``; steps outside every packed sequence are not written."""
+    if stream is None:
+        both = _marshal.scan(_SCAN, x, r, i, lam, r_bias, i_bias, z, c, h0, cu_seqlens, out, last_state, return_last_state)
+        if type(both) is int:
+            _check(both)
+        return both
     if out is None or (last_state is None and return_last_state):
         with _allocating_on(stream, x.device):
             if out is None:
@@ -495,6 +503,11 @@ def gated_scan_bwd(x, r, i, lam, r_bias=None, i_bias=None, z=None, dout=None, c=
     """Allocate the gradients with torch and run the gated recurrence's backward pass: ``dx, dr, di, dz,
     dlam, dr_bias, di_bias, dh0`` (None where the input is; ``dh0`` is given with ``h0``).  Gradients at steps
     outside every packed sequence are not written."""
+    if stream is None:
+        g = _marshal.scan_bwd(_SCAN_BWD, x, r, i, lam, r_bias, i_bias, z, c, h0, cu_seqlens, dout, dlast_state)
+        if type(g) is int:
+            _check(g)
+        return dict(zip(_GRADS, g))
     device, f32 = x.device, torch.float32
     batch, dim = x.shape[0], x.shape[1]
     with _allocating_on(stream, device):

@@ -1,7 +1,9 @@
-// The Python binding's fast part: writes a call's tensor descriptors, and makes the decode path's two calls.
+// The Python binding's fast part: writes a call's tensor descriptors, allocates its outputs and makes the call.
 // A decode step is a few microseconds on the GPU; reading eight tensors' pointers, shapes and strides from
 // Python takes longer than that.
 #include <Python.h>
+
+#include <algorithm>
 
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -97,7 +99,7 @@ PyObject* describe(PyObject* const* args, Py_ssize_t n) {
 
 // Descriptors of a call's tensors, and the call itself on the device's current stream.
 struct Call {
-  mssm_tensor d[9];
+  mssm_tensor d[20];
   int device = -1;
   int used = 0;
   // null for None; `ok` turns false with a Python error
@@ -163,6 +165,101 @@ PyObject* step(PyObject* const* args, Py_ssize_t n) {
   return call.run(made, [&](void* s) { return fn(state, x, r, i, lam, rb, ib, z, float(c), out, s); });
 }
 
+// scan(function, x, r, i, lam, r_bias, i_bias, z, decay scale, h0, cu_seqlens, out, last_state, whether to return it)
+// -> (out, last_state), or the status of a failed call
+PyObject* scan(PyObject* const* args, Py_ssize_t n) {
+  if (n != 14) {
+    PyErr_SetString(PyExc_TypeError, "scan takes 14 arguments");
+    return nullptr;
+  }
+  const auto fn = reinterpret_cast<decltype(&mssm_gated_scan_fwd)>(PyLong_AsVoidPtr(args[0]));
+  const double c = PyFloat_AsDouble(args[8]);
+  const int want = PyObject_IsTrue(args[13]);
+  if (!fn || want < 0 || PyErr_Occurred()) return nullptr;
+  Call call;
+  const mssm_tensor* t[7];
+  for (int k = 0; k < 7; ++k) t[k] = call.in(args[1 + k]);
+  const mssm_gated_ext ext{int32_t(sizeof(mssm_gated_ext)), float(c), call.in(args[9]), call.in(args[10])};
+  if (!call.ok) return nullptr;
+  if (!t[0] || t[0]->ndim != 3) {
+    PyErr_SetString(PyExc_ValueError, "x: expected [Bt, D, L]");
+    return nullptr;
+  }
+  const at::Tensor& x = THPVariable_Unpack(args[1]);
+  const int64_t seqs = ext.cu_seqlens ? std::max<int64_t>(ext.cu_seqlens->shape[0] - 1, 0) : x.size(0);
+  PyObject* both = PyTuple_New(2);
+  if (!both) return nullptr;
+  PyObject *out_made = nullptr, *last_made = nullptr;
+  mssm_tensor* out = call.out(args[11], out_made, [&] { return at::empty(x.sizes(), x.options().requires_grad(false)); });
+  PyTuple_SET_ITEM(both, 0, out_made);
+  mssm_tensor* last = nullptr;
+  if (want || args[12] != Py_None) {
+    last = call.out(args[12], last_made, [&] {
+      return at::empty({seqs, x.size(1)}, x.options().dtype(at::kFloat).requires_grad(false));
+    });
+  } else {
+    Py_INCREF(Py_None);
+    last_made = Py_None;
+  }
+  PyTuple_SET_ITEM(both, 1, last_made);
+  return call.run(both, [&](void* s) { return fn(t[0], t[1], t[2], t[3], t[4], t[5], t[6], &ext, out, last, s); });
+}
+
+// scan_bwd(function, x, r, i, lam, r_bias, i_bias, z, decay scale, h0, cu_seqlens, dout, dlast_state) -> (dx, dr, di,
+// dz, dlam, dr_bias, di_bias, dh0), or the status of a failed call
+PyObject* scan_bwd(PyObject* const* args, Py_ssize_t n) {
+  if (n != 13) {
+    PyErr_SetString(PyExc_TypeError, "scan_bwd takes 13 arguments");
+    return nullptr;
+  }
+  const auto fn = reinterpret_cast<decltype(&mssm_gated_scan_bwd)>(PyLong_AsVoidPtr(args[0]));
+  const double c = PyFloat_AsDouble(args[8]);
+  if (!fn || PyErr_Occurred()) return nullptr;
+  Call call;
+  const mssm_tensor* t[7];
+  for (int k = 0; k < 7; ++k) t[k] = call.in(args[1 + k]);
+  const mssm_gated_ext ext{int32_t(sizeof(mssm_gated_ext)), float(c), call.in(args[9]), call.in(args[10])};
+  const mssm_tensor *dout = call.in(args[11]), *dlast = call.in(args[12]);
+  if (!call.ok) return nullptr;
+  if (!t[0] || t[0]->ndim != 3) {
+    PyErr_SetString(PyExc_ValueError, "x: expected [Bt, D, L]");
+    return nullptr;
+  }
+  const at::Tensor& x = THPVariable_Unpack(args[1]);
+  const auto like = x.options().requires_grad(false), f32 = like.dtype(at::kFloat);
+  PyObject* made = PyTuple_New(8);
+  if (!made) return nullptr;
+  mssm_tensor* g[8];
+  for (int k = 0; k < 8; ++k) {
+    // dz, the biases' gradients and dh0 come with their inputs
+    const bool on = k == 3 ? t[6] != nullptr : k == 5 ? t[4] != nullptr : k == 6 ? t[5] != nullptr : k == 7 ? ext.h0 != nullptr : true;
+    PyObject* one = nullptr;
+    if (on) {
+      g[k] = call.out(Py_None, one, [&] {
+        if (k < 4) return at::empty(x.sizes(), like);
+        if (k < 7) return at::empty({x.size(1)}, f32);
+        return at::empty(THPVariable_Unpack(args[9]).sizes(), f32);
+      });
+    } else {
+      g[k] = nullptr;
+      Py_INCREF(Py_None);
+      one = Py_None;
+    }
+    PyTuple_SET_ITEM(made, k, one);
+  }
+  mssm_tensor ws{};
+  at::Tensor sums;
+  if (x.size(0) > 1) {
+    sums = at::empty({3, x.size(0), x.size(1)}, f32);
+    ws = mssm_tensor{sums.numel() ? sums.data_ptr() : nullptr, MSSM_F32, 3, {3, x.size(0), x.size(1), 0},
+                     {sums.stride(0), sums.stride(1), sums.stride(2), 0}};
+  }
+  return call.run(made, [&](void* s) {
+    return fn(t[0], t[1], t[2], t[3], t[4], t[5], t[6], &ext, dout, dlast, g[0], g[1], g[2], g[3], g[4], g[5], g[6], g[7],
+              sums.defined() ? &ws : nullptr, s);
+  });
+}
+
 // linear(function, x, qweight, qscales, qzeros, group, bias, outputs, out) -> out, or the status of a failed call
 PyObject* linear(PyObject* const* args, Py_ssize_t n) {
   if (n != 9) {
@@ -204,6 +301,12 @@ PyMethodDef methods[] = {
     {"describe", method<describe>(), METH_FASTCALL, "describe(block, *tensors) -> (device index, *descriptor addresses)"},
     {"step", method<step>(), METH_FASTCALL,
      "step(function, state, x, r, i, lam, r_bias, i_bias, z, decay_scale, out) -> out, or a failed call's status"},
+    {"scan", method<scan>(), METH_FASTCALL,
+     "scan(function, x, r, i, lam, r_bias, i_bias, z, decay_scale, h0, cu_seqlens, out, last_state, want_last) -> "
+     "(out, last_state), or a failed call's status"},
+    {"scan_bwd", method<scan_bwd>(), METH_FASTCALL,
+     "scan_bwd(function, x, r, i, lam, r_bias, i_bias, z, decay_scale, h0, cu_seqlens, dout, dlast_state) -> gradients, or "
+     "a failed call's status"},
     {"linear", method<linear>(), METH_FASTCALL,
      "linear(function, x, qweight, qscales, qzeros, group, bias, outputs, out) -> out, or a failed call's status"},
     {nullptr, nullptr, 0, nullptr}};
