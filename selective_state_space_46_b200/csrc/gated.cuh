@@ -288,9 +288,6 @@ __device__ __forceinline__ void step_pair_grad(f2_t& x, f2_t& rr, f2_t& ii, f2_t
 constexpr int kH = kGs / 2;
 
 __device__ __forceinline__ float of(const f2_t (&f)[kH], int e) { return e < kH ? f2lo(f[e]) : f2hi(f[e - kH]); }
-__device__ __forceinline__ void set(f2_t (&f)[kH], int e, float v) {
-  f[e % kH] = e < kH ? f2(v, f2hi(f[e])) : f2(f2lo(f[e - kH]), v);
-}
 // 1 for the steps of `mask` and 0 for the others
 __device__ __forceinline__ f2_t ones(unsigned mask, int k) {
   return f2(mask >> k & 1u ? 1.0f : 0.0f, mask >> (k + kH) & 1u ? 1.0f : 0.0f);
@@ -634,6 +631,170 @@ struct GatedPlace {
   }
 };
 
+// A window in which no thread has more than one first and one last step: selected step by step, without a branch.
+// The warp at a boundary holds up the other warps of its row, so what counts here is the way through.
+__device__ __forceinline__ bool on_bit(unsigned mask, int e) { return mask >> e & 1u; }
+
+// The map (A, B); the steps outside the sequences become the identity, and the first step's b takes h0.
+__device__ __forceinline__ float2 edge_map(f2_t (&a)[kH], f2_t (&b)[kH], const SeqMask& m, float h0) {
+  float av[kGs], bv[kGs], A = 1.0f, B = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kH; ++k) {
+    f2split(a[k], av[k], av[k + kH]);
+    f2split(b[k], bv[k], bv[k + kH]);
+  }
+#pragma unroll
+  for (int e = 0; e < kGs; ++e) {
+    if (!on_bit(m.valid, e)) av[e] = 1.0f, bv[e] = 0.0f;
+    if (on_bit(m.first, e)) bv[e] = fmaf(av[e], h0, bv[e]);
+    const float through = fmaf(av[e], B, bv[e]);
+    B = on_bit(m.first, e) ? bv[e] : through;
+    A *= av[e];
+  }
+#pragma unroll
+  for (int k = 0; k < kH; ++k) {
+    a[k] = f2(av[k], av[k + kH]);
+    b[k] = f2(bv[k], bv[k + kH]);
+  }
+  return make_float2(m.first ? kResetA : A, B);
+}
+// The states after every step (in b) and, with BEFORE, before it; returns that of the last step.
+template <bool BEFORE>
+__device__ __forceinline__ float edge_states(const f2_t (&a)[kH], f2_t (&b)[kH], const SeqMask& m, float h, float h0,
+                                             f2_t (&before)[kH]) {
+  float out[kGs], pre[kGs], last = 0.0f;
+#pragma unroll
+  for (int e = 0; e < kGs; ++e) {
+    if (BEFORE) pre[e] = !on_bit(m.valid, e) ? 0.0f : on_bit(m.first, e) ? h0 : h;
+    const float through = fmaf(of(a, e), h, of(b, e));
+    h = on_bit(m.first, e) ? of(b, e) : through;
+    if (on_bit(m.last, e)) last = h;
+    out[e] = BEFORE && !on_bit(m.valid, e) ? 0.0f : h;
+  }
+#pragma unroll
+  for (int k = 0; k < kH; ++k) {
+    b[k] = f2(out[k], out[k + kH]);
+    if (BEFORE) before[k] = f2(pre[k], pre[k + kH]);
+  }
+  return last;
+}
+// The adjoint's map; the last step's g takes dlast.
+__device__ __forceinline__ float2 edge_adjoint_map(const f2_t (&a)[kH], f2_t (&g)[kH], const SeqMask& m, float dlast) {
+  float gv[kGs], A = 1.0f, B = 0.0f;
+#pragma unroll
+  for (int e = kGs - 1; e >= 0; --e) {
+    gv[e] = of(g, e);
+    if (on_bit(m.last, e)) gv[e] += dlast;
+    B = of(a, e) * (on_bit(m.last, e) ? gv[e] : gv[e] + B);
+    A *= of(a, e);
+  }
+#pragma unroll
+  for (int k = 0; k < kH; ++k) g[k] = f2(gv[k], gv[k + kH]);
+  return make_float2(m.last ? kResetA : A, B);
+}
+// The adjoint at every step; returns what flows into the state before the first step.
+__device__ __forceinline__ float edge_adjoint(const f2_t (&a)[kH], const f2_t (&g)[kH], const SeqMask& m, float c, f2_t (&s)[kH]) {
+  float sv[kGs], first = 0.0f;
+#pragma unroll
+  for (int e = kGs - 1; e >= 0; --e) {
+    const float se = on_bit(m.last, e) ? of(g, e) : of(g, e) + c;
+    c = of(a, e) * se;
+    if (on_bit(m.first, e)) first = c;
+    sv[e] = on_bit(m.valid, e) ? se : 0.0f;  // what flows past the steps outside stays out of the sums
+  }
+#pragma unroll
+  for (int k = 0; k < kH; ++k) s[k] = f2(sv[k], sv[k + kH]);
+  return first;
+}
+
+__device__ __forceinline__ bool several(const SeqMask& m) {
+  return (m.first & (m.first - 1u)) != 0u || (m.last & (m.last - 1u)) != 0u;
+}
+
+// A window with more boundaries than that, a thread's steps in local memory: sequences of a few steps.
+struct BoundWin {
+  float a[kGs], b[kGs];         // the steps' maps; b becomes the states
+  float before[kGs], g[kGs];    // backward: the state before each step; dout silu(z), which becomes the adjoint
+  SeqMask m;
+  SeqWalk walk;
+  int t0;
+  // a state per sequence, at step e, where the one at `early` is known
+  __device__ float state(const float* p, int64_t sb, int e, int early, float known) const {
+    return !p ? 0.0f : e == early ? known : p[int64_t(walk.seq(m, t0, e)) * sb];
+  }
+  __device__ __forceinline__ void take(const f2_t (&av)[kH], const f2_t (&bv)[kH], const SeqMask& m_, const SeqWalk& walk_, int t) {
+    m = m_;
+    walk = walk_;
+    t0 = t;
+#pragma unroll
+    for (int k = 0; k < kH; ++k) {
+      f2split(av[k], a[k], a[k + kH]);
+      f2split(bv[k], b[k], b[k + kH]);
+    }
+  }
+};
+
+// Forward: the window's map.  h0: of this channel.
+static __device__ __noinline__ float2 bound_map(BoundWin& w, const float* h0, int64_t sb, float h0_first) {
+  float A = 1.0f, B = 0.0f;
+  const int early = __ffs(w.m.first) - 1;
+#pragma unroll 1
+  for (int e = 0; e < kGs; ++e) {
+    float a = w.a[e], b = w.b[e];
+    w.before[e] = 0.0f;
+    if (!(w.m.valid >> e & 1u)) a = 1.0f, b = 0.0f;
+    if (w.m.first >> e & 1u) {
+      w.before[e] = w.state(h0, sb, e, early, h0_first);
+      b = fmaf(a, w.before[e], b);
+      a = kResetA;
+    }
+    compose<true>(a, b, A, B);
+    A = a;
+    B = b;
+  }
+  return make_float2(A, B);
+}
+
+// The states from the one before the window; `last`: of this channel, written at the sequences' ends.
+static __device__ __noinline__ void bound_states(BoundWin& w, float h, float* last, int64_t sb) {
+#pragma unroll 1
+  for (int e = 0; e < kGs; ++e) {
+    const bool valid = w.m.valid >> e & 1u;
+    if (!(w.m.first >> e & 1u)) w.before[e] = h;
+    if (valid) h = fmaf(w.a[e], w.before[e], w.b[e]);
+    if (!valid) w.before[e] = 0.0f;  // outside every sequence
+    w.b[e] = valid ? h : 0.0f;
+    if ((w.m.last >> e & 1u) && last) last[int64_t(w.walk.seq(w.m, w.t0, e)) * sb] = h;
+  }
+}
+
+// Backward: the adjoint's map, dlast added to g at the sequences' ends.
+static __device__ __noinline__ float2 bound_adjoint_map(BoundWin& w, const float* dlast, int64_t sb, float dl_last) {
+  float A = 1.0f, B = 0.0f;
+  const int early = 31 - __clz(w.m.last);
+#pragma unroll 1
+  for (int e = kGs - 1; e >= 0; --e) {
+    const bool end = w.m.last >> e & 1u;
+    if (end) w.g[e] += w.state(dlast, sb, e, early, dl_last);
+    float a = end ? kResetA : w.a[e], b = w.a[e] * w.g[e];
+    compose<true>(a, b, A, B);
+    A = a;
+    B = b;
+  }
+  return make_float2(A, B);
+}
+
+// The adjoint from what flows into the window's end.
+static __device__ __noinline__ void bound_adjoint(BoundWin& w, float c, float* dh0, int64_t sb) {
+#pragma unroll 1
+  for (int e = kGs - 1; e >= 0; --e) {
+    const float s = w.m.last >> e & 1u ? w.g[e] : w.g[e] + c;
+    c = w.a[e] * s;
+    if ((w.m.first >> e & 1u) && dh0) dh0[int64_t(w.walk.seq(w.m, w.t0, e)) * sb] = c;
+    w.g[e] = w.m.valid >> e & 1u ? s : 0.0f;  // what flows past the steps outside stays out of the sums
+  }
+}
+
 // The map of a window whose steps all count: of its halves, and of all (A, B).
 struct WinMap {
   float a_lo, b_lo, a_hi, b_hi;
@@ -753,31 +914,26 @@ __global__ void __launch_bounds__(gated_threads(W), kScanWarps * 32 / gated_thre
         o[k] = Z ? mul2(hh, zv[k]) : hh;
       }
     } else {
-      float A = 1.0f, B = 0.0f;
-#pragma unroll
-      for (int e = 0; e < kGs; ++e) {
-        float ca = of(a, e), cb = of(b, e);
-        if (!(m.valid >> e & 1u)) ca = 1.0f, cb = 0.0f;
-        if (m.first >> e & 1u) {
-          if (p.h0) {
-            const bool early = (m.first & ((1u << e) - 1u)) == 0u;
-            cb = fmaf(ca, early ? h0_first : p.h0[int64_t(walk.seq(m, t0, e)) * p.h0_sb + d * p.h0_sd], cb);
-          }
-          ca = kResetA;
-        }
-        set(a, e, ca);
-        set(b, e, cb);
-        compose<VL>(ca, cb, A, B);
-        A = ca;
-        B = cb;
+      const bool few = !__any_sync(~0u, several(m));
+      BoundWin bw;
+      float2 map;
+      if (few) {
+        map = edge_map(a, b, m, h0_first);
+      } else {
+        bw.take(a, b, m, walk, t0);
+        map = bound_map(bw, p.h0 ? p.h0 + d * p.h0_sd : nullptr, p.h0_sb, h0_first);
       }
-      float hk = tile_carry<VL, false, W, CL>(A, B, h, sm, flip, at.wc, lane, at.rank, at.split, whole);
+      const float in = tile_carry<VL, false, W, CL>(map.x, map.y, h, sm, flip, at.wc, lane, at.rank, at.split, whole);
+      if (few) {
+        const float last = edge_states<false>(a, b, m, in, h0_first, b);
+        if (m.last && p.last) p.last[int64_t(walk.seq(m, t0, 31 - __clz(m.last))) * p.ls_sb + d * p.ls_sd] = last;
+      } else {
+        bound_states(bw, in, p.last ? p.last + d * p.ls_sd : nullptr, p.ls_sb);
 #pragma unroll
-      for (int e = 0; e < kGs; ++e) {
-        hk = apply<VL>(of(a, e), of(b, e), hk);
-        if ((m.last >> e & 1u) && p.last) p.last[int64_t(walk.seq(m, t0, e)) * p.ls_sb + d * p.ls_sd] = hk;
-        set(o, e, Z ? hk * of(zv, e) : hk);
+        for (int k = 0; k < kH; ++k) b[k] = f2(bw.b[k], bw.b[k + kH]);
       }
+#pragma unroll
+      for (int k = 0; k < kH; ++k) o[k] = Z ? mul2(b[k], zv[k]) : b[k];
     }
     win_store(out, wt, lane, m.valid, vec && inner, o);
   }
@@ -868,11 +1024,6 @@ __global__ void __launch_bounds__(gated_threads(W), kBwdWarps * 32 / gated_threa
     if (VL && m.first && p.h0)
       h0_first = p.h0[int64_t(walk.seq(m, wt + lane * kGs, __ffs(m.first) - 1)) * p.h0_sb + d * p.h0_sd];
   };
-  auto h0_at = [&](int t0, int e) {
-    if (!p.h0) return 0.0f;
-    const bool early = (m.first & ((1u << e) - 1u)) == 0u;
-    return early ? h0_first : p.h0[int64_t(walk.seq(m, t0, e)) * p.h0_sb + d * p.h0_sd];
-  };
   f2_t xv[kH], rv[kH], iv[kH], zv[kH], gv[kH], a[kH], b[kH];
   // steps outside count as zeros, whatever the tensors hold there
   auto unpack = [&] {
@@ -892,6 +1043,16 @@ __global__ void __launch_bounds__(gated_threads(W), kBwdWarps * 32 / gated_threa
     if (!whole) {
       blank(gv, m.valid);
       if (Z) blank(zv, m.valid);
+    }
+  };
+
+  // the identity outside: y = 0, a = 1 (b is 0 with x)
+  auto identity_outside = [&] {
+#pragma unroll
+    for (int k = 0; k < kH; ++k) {
+      const f2_t on = ones(m.valid, k);
+      xv[k] = mul2(xv[k], on);
+      a[k] = fma2(a[k], on, fma2(on, f2s(-1.0f), f2s(1.0f)));
     }
   };
 
@@ -917,24 +1078,23 @@ __global__ void __launch_bounds__(gated_threads(W), kBwdWarps * 32 / gated_threa
 #pragma unroll
       for (int k = 0; k < kH; ++k) step_pair<false, true>(xv[k], rv[k], iv[k], 0, w, a[k], b[k], none, most);
     }
-    float A = 1.0f, B = 0.0f;
-    if (whole) {
+    float A, B;
+    if (!VL || whole) {
+      if (!VL && !whole) identity_outside();
       const WinMap wm = win_map(a, b);
       A = wm.A;
       B = wm.B;
     } else {
-#pragma unroll
-      for (int e = 0; e < kGs; ++e) {
-        float ca = of(a, e), cb = of(b, e);
-        if (!(m.valid >> e & 1u)) ca = 1.0f, cb = 0.0f;
-        if (VL && (m.first >> e & 1u)) {
-          cb = fmaf(ca, h0_at(t0, e), cb);
-          ca = kResetA;
-        }
-        compose<VL>(ca, cb, A, B);
-        A = ca;
-        B = cb;
+      float2 map;
+      if (!__any_sync(~0u, several(m))) {
+        map = edge_map(a, b, m, h0_first);
+      } else {
+        BoundWin bw;
+        bw.take(a, b, m, walk, t0);
+        map = bound_map(bw, p.h0 ? p.h0 + d * p.h0_sd : nullptr, p.h0_sb, h0_first);
       }
+      A = map.x;
+      B = map.y;
     }
     tile_carry<VL, false, W, CL>(A, B, h, sm, flip, wc, lane, rank, split, whole);
   }
@@ -967,14 +1127,7 @@ __global__ void __launch_bounds__(gated_threads(W), kBwdWarps * 32 / gated_threa
       for (int k = 0; k < kH; ++k)
         step_pair_grad<Z, true>(xv[k], rv[k], iv[k], zv[k], gv[k], w, a[k], b[k], pv[k], cv[k], most);
     }
-    if (!whole) {
-#pragma unroll
-      for (int k = 0; k < kH; ++k) {  // the identity outside: y = 0, a = 1 (b is 0 with x)
-        const f2_t on = ones(m.valid, k);
-        xv[k] = mul2(xv[k], on);
-        a[k] = fma2(a[k], on, fma2(on, f2s(-1.0f), f2s(1.0f)));
-      }
-    }
+    if (!whole) identity_outside();
     // now xv: -y, rv: 1 - r, iv: i x rho, zv: dout silu'(z), gv: dout silu(z)
     f2_t s[kH];
     float hin = ckpt[tl];
@@ -1003,57 +1156,48 @@ __global__ void __launch_bounds__(gated_threads(W), kBwdWarps * 32 / gated_threa
         cc = mul2(a[k], s[k]);
       }
     } else {
-      float hb[kGs], A = 1.0f, B = 0.0f;
-#pragma unroll
-      for (int e = 0; e < kGs; ++e) {
-        hb[e] = 0.0f;
-        float ca = of(a, e), cb = of(b, e);
-        if (m.first >> e & 1u) {
-          hb[e] = h0_at(t0, e);
-          cb = fmaf(ca, hb[e], cb);
-          ca = kResetA;
-        }
-        compose<VL>(ca, cb, A, B);
-        A = ca;
-        B = cb;
+      const bool few = !__any_sync(~0u, several(m));
+      BoundWin bw;
+      f2_t before[kH];
+      float2 map;
+      if (few) {
+        map = edge_map(a, b, m, h0_first);
+      } else {
+        bw.take(a, b, m, walk, t0);
+        map = bound_map(bw, p.h0 ? p.h0 + d * p.h0_sd : nullptr, p.h0_sb, h0_first);
       }
-      float hk = tile_carry<VL, false, W, CL>(A, B, hin, sm, flip, wc, lane, rank, split, whole);
+      const float in = tile_carry<VL, false, W, CL>(map.x, map.y, hin, sm, flip, wc, lane, rank, split, whole);
+      if (few) {
+        edge_states<true>(a, b, m, in, h0_first, before);
+      } else {
+        bound_states(bw, in, nullptr, 0);
 #pragma unroll
-      for (int e = 0; e < kGs; ++e) {
-        if (!(m.first >> e & 1u)) hb[e] = hk;
-        hk = fmaf(of(a, e), hb[e], of(b, e));
-        if (!(m.valid >> e & 1u)) hk = hb[e] = 0.0f;  // outside every sequence
-        set(b, e, hk);
+        for (int k = 0; k < kH; ++k) {
+          before[k] = f2(bw.before[k], bw.before[k + kH]);
+          b[k] = f2(bw.b[k], bw.b[k + kH]);
+        }
       }
 #pragma unroll
       for (int k = 0; k < kH; ++k) {
-        xv[k] = mul2(a[k], fma2(xv[k], f2(hb[k], hb[k + kH]), iv[k]));
+        xv[k] = mul2(a[k], fma2(xv[k], before[k], iv[k]));
         if (Z) zv[k] = mul2(zv[k], b[k]);
       }
-      A = 1.0f;
-      B = 0.0f;
-#pragma unroll
-      for (int e = kGs - 1; e >= 0; --e) {
-        float g = of(gv, e);
-        const bool end = m.last >> e & 1u;
-        if (end && p.dlast) {
-          const bool early = (m.last >> e) == 1u;
-          g += early ? dl_last : p.dlast[int64_t(walk.seq(m, t0, e)) * p.dl_sb + d * p.dl_sd];
-          set(gv, e, g);
-        }
-        float ca = end ? kResetA : of(a, e), cb = of(a, e) * g;
-        compose<VL>(ca, cb, A, B);
-        A = ca;
-        B = cb;
-      }
       if (Z) win_store(dz, wt, lane, m.valid, inner, zv);
-      float ck = tile_carry<VL, true, W, CL>(A, B, c, sm, flip, wc, lane, rank, split, whole);
+      if (few) {
+        map = edge_adjoint_map(a, gv, m, dl_last);
+      } else {
 #pragma unroll
-      for (int e = kGs - 1; e >= 0; --e) {
-        const float g = of(gv, e), se = m.last >> e & 1u ? g : g + ck;
-        ck = of(a, e) * se;
-        if ((m.first >> e & 1u) && p.dh0) p.dh0[int64_t(walk.seq(m, t0, e)) * p.dh_sb + d * p.dh_sd] = ck;
-        set(s, e, m.valid >> e & 1u ? se : 0.0f);  // what flows past the steps outside stays out of the sums
+        for (int k = 0; k < kH; ++k) f2split(gv[k], bw.g[k], bw.g[k + kH]);
+        map = bound_adjoint_map(bw, p.dlast ? p.dlast + d * p.dl_sd : nullptr, p.dl_sb, dl_last);
+      }
+      const float cin = tile_carry<VL, true, W, CL>(map.x, map.y, c, sm, flip, wc, lane, rank, split, whole);
+      if (few) {
+        const float first = edge_adjoint(a, gv, m, cin, s);
+        if (m.first && p.dh0) p.dh0[int64_t(walk.seq(m, t0, __ffs(m.first) - 1)) * p.dh_sb + d * p.dh_sd] = first;
+      } else {
+        bound_adjoint(bw, cin, p.dh0 ? p.dh0 + d * p.dh_sd : nullptr, p.dh_sb);
+#pragma unroll
+        for (int k = 0; k < kH; ++k) s[k] = f2(bw.g[k], bw.g[k + kH]);
       }
     }
 #pragma unroll
