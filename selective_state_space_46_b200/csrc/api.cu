@@ -1279,6 +1279,8 @@ mssm_status gated_prepare(const mssm_tensor* x, const mssm_tensor* r, const mssm
 //  * as many warps as keep all rows' warps within 70 per SM (three rounds of resident CTAs): 5120x4096
 //    with 1 / 2 / 4 / 8 warps 55 / 51 / 51 / 61 and 131 / 115 / 115 / 133, 1536x16384 76 / 68 / 61 / 66 and
 //    184 / 162 / 143 / 154, 300x32768 104 / 64 / 41 / 39; and no more than the length fills (8192x256: 14 / 23 / 37 / 76);
+//  * eight warps of the backward pass, whose CTAs of 32 K registers are two to an SM, within 24 per SM (513x10007
+//    packed fp32 with 4 / 8 warps 61 / 68; 148x65536 119 / 82);
 //  * two warps for long rows however many there are: 40960x4096 backward with 1 / 2 / 4 warps 866 / 786 / 821;
 //  * a cluster only while its CTAs' warps stay within 14 per SM and each keeps two tiles or more: 16x131072 in
 //    1 / 2 / 4 / 8 CTAs 68 / 68 / 37 / 25, 64x65536 37 / 39 / 25 / 27, but 148x65536 39 / 45 / 49 / 49.
@@ -1286,11 +1288,11 @@ struct GatedShape {
   int warps, split;
 };
 
-GatedShape gated_shape(int64_t rows, int64_t L, int sms) {
+GatedShape gated_shape(int64_t rows, int64_t L, bool backward, int sms) {
   const int64_t step = 32 * mssm::kGs;  // steps of a warp
   GatedShape g{1, 1};
   while (g.warps < 8 && g.warps * step < L &&
-         (rows * g.warps * 2 <= int64_t(70) * sms || (g.warps == 1 && L >= 8 * step)))
+         (rows * g.warps * 2 <= int64_t(backward && g.warps == 4 ? 24 : 70) * sms || (g.warps == 1 && L >= 8 * step)))
     g.warps *= 2;
   while (g.warps == 8 && g.split < mssm::kMaxSplit && rows * 8 * g.split * 2 <= int64_t(14) * sms &&
          L >= 8 * step * 4 * g.split)
@@ -1330,7 +1332,7 @@ mssm_status mssm_gated_scan_fwd(const mssm_tensor* x, const mssm_tensor* r, cons
   if (e != cudaSuccess) return cuda_fail(e, "device error word");
   int dev = -1;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  const GatedShape g = gated_shape(call.Bt * call.D, call.L, device_state(dev)->sm_count);
+  const GatedShape g = gated_shape(call.Bt * call.D, call.L, false, device_state(dev)->sm_count);
   a.split = g.split;
   e = tracked(MSSM_KERNEL_GATED_SCAN, s, [&] { return mssm::launch_gated_scan(a, g.warps, call.dtype, s); });
   if (e != cudaSuccess) return cuda_fail(e, "gated scan kernel launch");
@@ -1398,7 +1400,7 @@ mssm_status mssm_gated_scan_bwd(const mssm_tensor* x, const mssm_tensor* r, cons
   if (e != cudaSuccess) return cuda_fail(e, "device error word");
   int dev = -1;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  GatedShape g = gated_shape(call.Bt * call.D, call.L, device_state(dev)->sm_count);
+  GatedShape g = gated_shape(call.Bt * call.D, call.L, true, device_state(dev)->sm_count);
   if (call.L > (1 << 19) && g.warps < 8) g.warps = 8;  // the checkpoints of a CTA's rows fit 48 KB
   a.split = g.split;
   const int64_t tile = int64_t(32) * g.warps * g.split * mssm::kGs;

@@ -884,14 +884,18 @@ __global__ void __launch_bounds__(gated_threads(W), kScanWarps * 32 / gated_thre
     unpack();
     if (base + tile < p.L) fetch(wt + tile);
     f2_t most = 0;
-    if (!w.slow) {
+    bool care = w.slow;
+    if (!care) {
 #pragma unroll
       for (int k = 0; k < kH; ++k) step_pair<Z, false>(xv[k], rv[k], iv[k], zv[k], w, a[k], b[k], zv[k], most);
+      care = __any_sync(~0u, !in_range(most));
+      if (care) {
+        fetch(wt);
+        unpack();
+        if (base + tile < p.L) fetch(wt + tile);
+      }
     }
-    if (w.slow || __any_sync(~0u, !in_range(most))) {
-      fetch(wt);
-      unpack();
-      if (base + tile < p.L) fetch(wt + tile);
+    if (care) {
 #pragma unroll
       for (int k = 0; k < kH; ++k) step_pair<Z, true>(xv[k], rv[k], iv[k], zv[k], w, a[k], b[k], zv[k], most);
     }
@@ -1066,15 +1070,19 @@ __global__ void __launch_bounds__(gated_threads(W), kBwdWarps * 32 / gated_threa
     if (tl + 2 < ntiles) fetch(wt + tile);
     else fetch_all(wt + tile);
     f2_t most = 0, none;
-    if (!w.slow) {
+    bool care = w.slow;
+    if (!care) {
 #pragma unroll
       for (int k = 0; k < kH; ++k) step_pair<false, false>(xv[k], rv[k], iv[k], 0, w, a[k], b[k], none, most);
+      care = __any_sync(~0u, !in_range(most));
+      if (care) {
+        fetch(wt);
+        unpack();
+        if (tl + 2 < ntiles) fetch(wt + tile);
+        else fetch_all(wt + tile);
+      }
     }
-    if (w.slow || __any_sync(~0u, !in_range(most))) {
-      fetch(wt);
-      unpack();
-      if (tl + 2 < ntiles) fetch(wt + tile);
-      else fetch_all(wt + tile);
+    if (care) {
 #pragma unroll
       for (int k = 0; k < kH; ++k) step_pair<false, true>(xv[k], rv[k], iv[k], 0, w, a[k], b[k], none, most);
     }
@@ -1114,15 +1122,19 @@ __global__ void __launch_bounds__(gated_threads(W), kBwdWarps * 32 / gated_threa
     unpack_all();
     if (tl > 0) fetch_all(wt - tile);
     f2_t pv[kH], cv[kH], most = 0;
-    if (!w.slow) {
+    bool care = w.slow;
+    if (!care) {
 #pragma unroll
       for (int k = 0; k < kH; ++k)
         step_pair_grad<Z, false>(xv[k], rv[k], iv[k], zv[k], gv[k], w, a[k], b[k], pv[k], cv[k], most);
+      care = __any_sync(~0u, !in_range(most));
+      if (care) {
+        fetch_all(wt);
+        unpack_all();
+        if (tl > 0) fetch_all(wt - tile);
+      }
     }
-    if (w.slow || __any_sync(~0u, !in_range(most))) {
-      fetch_all(wt);
-      unpack_all();
-      if (tl > 0) fetch_all(wt - tile);
+    if (care) {
 #pragma unroll
       for (int k = 0; k < kH; ++k)
         step_pair_grad<Z, true>(xv[k], rv[k], iv[k], zv[k], gv[k], w, a[k], b[k], pv[k], cv[k], most);
