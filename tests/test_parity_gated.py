@@ -490,3 +490,117 @@ def test_launches_are_counted(cuda_device):
     m.gated_scan_bwd(*args(d), dout=d["x"])
     after = {k: v["launches"] for k, v in m.mssm_kernel_stats().items()}
     assert after["gated_scan"] == before["gated_scan"] + 1 and after["gated_bwd"] == before["gated_bwd"] + 1
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("packed", [False, True])
+def test_spikes_among_ordinary_gates(cuda_device, io, packed):
+    """Now and then a gate so far from zero that its window is computed with more care, over many tiles."""
+    L = 9001
+    cu = [0, 700, 701, 4096, 8000, L] if packed else None
+    p = ref.gated_inputs(1 if packed else 2, 5, L, io, h0=True, cu=cu, seed=21)
+    rng = np.random.default_rng(22)
+    for k in ("r", "i", "z"):
+        at = rng.random(p[k].shape) < 2e-3
+        p[k] = np.where(at, rng.choice([-80.0, -50.0, 50.0, 80.0], p[k].shape), p[k])
+    check_fwd(p, io)
+    check_bwd(p, io, dlast=True)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_rates_around_the_polynomials_ends(cuda_device, io):
+    """Rates just below and above 1/8 and 1/4 with gates that take them whole."""
+    p = ref.gated_inputs(2, 9, 3000, io, h0=True, seed=23)
+    rates = np.array([1e-4, 0.1, 0.1249, 0.1251, 0.2, 0.2499, 0.2501, 1.0, 30.0])
+    p["lam"] = np.float32(np.log(np.expm1(rates / p["c"]))).astype(np.float64)
+    p["r"][:, :, ::3] = 12.0
+    check_fwd(p, io)
+    check_bwd(p, io, dlast=True)
+
+
+def test_offsets_past_32_bits(cuda_device):
+    """Rows and batches more than 2^31 elements apart."""
+    import selective_state_space_46_b200 as m
+    far = 2 ** 31 + 8
+    buf = torch.zeros(far + 4096, device="cuda", dtype=torch.bfloat16)
+    p = ref.gated_inputs(1, 2, 600, "bf16", seed=24)
+    d = tensors(p, "bf16")
+    views = [buf.as_strided((1, 2, 600), (far, far, 1), 640 * n) for n in range(5)]
+    for v, k in zip(views, ("x", "r", "i", "z")):
+        v.copy_(d[k])
+    out, last = m.gated_scan_fwd(*views[:3], d["lam"], d["r_bias"], d["i_bias"], views[3], out=views[4])
+    want = m.gated_scan_fwd(*args(d))
+    assert out.data_ptr() == views[4].data_ptr() and torch.equal(views[4], want[0]) and torch.equal(last, want[1])
+    dout = torch.randn_like(d["x"])
+    views[4].copy_(dout)
+    g = m.gated_scan_bwd(*views[:3], d["lam"], d["r_bias"], d["i_bias"], views[3], dout=views[4])
+    h = m.gated_scan_bwd(*args(d), dout=dout)
+    assert all(torch.equal(g[k], h[k]) for k in g if g[k] is not None)
+    rows = [buf.as_strided((2, 128), (far, 1), 640 * n) for n in range(4)]
+    state = torch.randn(2, 128, device="cuda")
+    other = state.clone()
+    lam = torch.randn(128, device="cuda")
+    o = m.gated_state_update(state, *rows[:3], lam, z=rows[3])
+    assert torch.equal(o, m.gated_state_update(other, *[v.contiguous() for v in rows[:3]], lam, z=rows[3].contiguous()))
+    assert torch.equal(state, other)
+
+
+def test_outputs_given_and_left_out(cuda_device):
+    """The caller's outputs are the ones returned; inputs that require gradients make no outputs that do."""
+    import selective_state_space_46_b200 as m
+    d = tensors(ref.gated_inputs(2, 6, 333, "f32", h0=True, seed=25), "f32")
+    d["x"].requires_grad_(True)
+    out, last = torch.empty(2, 6, 333, device="cuda"), torch.empty(2, 6, device="cuda")
+    side = torch.cuda.Stream()
+    for stream in (None, side, side.cuda_stream):
+        got = m.gated_scan_fwd(*args(d), h0=d["h0"], out=out, last_state=last, stream=stream)
+        torch.cuda.synchronize()
+        assert got[0] is out and got[1] is last
+        new, none = m.gated_scan_fwd(*args(d), h0=d["h0"], return_last_state=False, stream=stream)
+        torch.cuda.synchronize()
+        assert none is None and torch.equal(new, out) and not new.requires_grad
+        state = d["h0"].clone()
+        step = [d[k][..., 0] for k in ("x", "r", "i")]
+        o = torch.empty(2, 6, device="cuda")
+        assert m.gated_state_update(state, *step, d["lam"], out=o, stream=stream) is o
+        state2 = d["h0"].clone()
+        o2 = m.gated_state_update(state2, *step, d["lam"], stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(o, o2) and torch.equal(state, state2) and not o2.requires_grad
+    with pytest.raises(m.MssmError):
+        m.gated_scan_fwd(*args(d), out=torch.empty(2, 6, 334, device="cuda"))
+    with pytest.raises(m.MssmError):
+        m.gated_state_update(state, *step, d["lam"][:5])
+    with pytest.raises(TypeError):
+        m.gated_state_update(state, *step, [1.0] * 6)
+    with pytest.raises(ValueError):
+        m.gated_scan_fwd(d["x"][0], d["r"], d["i"], d["lam"])
+
+
+@pytest.mark.parametrize("rows", [1, 2, 4])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 4), (7, 12), (5, 13), (64, 260)])
+def test_every_step_plan(cuda_device, rows, io, shape):
+    """The decode step with 1, 2 and 4 batch rows a thread, whatever the automatic choice is, and replayed."""
+    import selective_state_space_46_b200 as m
+    p = ref.gated_inputs(*shape, 1, io, h0=True, seed=rows)
+    d = tensors(p, io)
+    flat = [d[k][..., 0].contiguous() for k in ("x", "r", "i")] + [d[k] for k in ("lam", "r_bias", "i_bias")]
+    z = d["z"][..., 0].contiguous()
+    want = ref.forward(p, io)
+    try:
+        m.mssm_set_option(m.MSSM_OPT_GATED_STEP_ROWS, rows)
+        state = d["h0"].clone()
+        out = m.gated_state_update(state, *flat, z=z)
+        within(out[..., None], want["out"], "out")
+        within(state, want["last_state"], "state")
+        again = d["h0"].clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            replayed = m.gated_state_update(again, *flat, z=z)
+        again.copy_(d["h0"])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(replayed, out) and torch.equal(again, state)
+    finally:
+        m.mssm_set_option(m.MSSM_OPT_GATED_STEP_ROWS, 0)

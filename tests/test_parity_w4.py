@@ -192,3 +192,24 @@ def test_recurrent_block_decodes_as_it_prefills(cuda_device):
     got = torch.cat(got, 1).double().cpu().numpy()
     # four stages of at most some hundred fp32 roundings each, on values of order one: 4 * 256 * 2^-24 of the scale
     assert np.abs(got - y).max() <= 4 * 256 * 2.0 ** -24 * (1 + np.abs(y).max())
+
+
+@pytest.mark.parametrize("plan", [2, 8, 16])
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(1, 16, 64, 32), (5, 33, 1000, 96), (13, 100, 4096, 128), (40, 48, 2100, 64)])
+def test_every_plan(cuda_device, plan, io, shape):
+    """One or two tiles and 8 or 16 warps a CTA, whatever the automatic choice is: fewer blocks than warps, odd tiles."""
+    import selective_state_space_46_b200 as m
+    m_, n, k, group = shape
+    try:
+        m.mssm_set_option(m.MSSM_OPT_W4_PLAN, plan)
+        for zeros in (False, True):
+            check(m_, n, k, group, io, zeros=zeros, bias=zeros, seed=plan)
+            check(m_, n, k - 1, group, io, scale_io="f32", zeros=zeros, seed=plan + 1)
+    finally:
+        m.mssm_set_option(m.MSSM_OPT_W4_PLAN, 0)
+
+
+def test_scales_of_a_group_wider_than_the_input(cuda_device):
+    check(3, 20, 100, 224, zeros=True, seed=31)
+    check(3, 20, 100, 2 ** 20, "f32", seed=32)
