@@ -472,7 +472,7 @@ mssm_status mssm_get_error(void *stream);
  *     share a row of the gated scans; 0 automatic.
  *   MSSM_OPT_W4_PLAN (value 0, 2, 8 or 16): a CTA of the 4-bit linear map takes 32 outputs with 8
  *     warps (2) or 16 outputs with 8 or 16 warps, which split its inputs; 0 automatic.
- *   MSSM_OPT_GATED_STEP_ROWS (value 0, 1, 2 or 4): batch rows that a thread of the gated state
+ *   MSSM_OPT_GATED_STEP_ROWS (value 0, 1 or 2): batch rows that a thread of the gated state
  *     update takes; 0 automatic.
  * Unknown options or invalid values return MSSM_ERR_INVALID_ARG.
  */

@@ -393,8 +393,8 @@ mssm_status mssm_set_option(int option, int64_t value) {
       g_gated_split = int(value);
       return MSSM_OK;
     case MSSM_OPT_GATED_STEP_ROWS:
-      if (value != 0 && value != 1 && value != 2 && value != 4)
-        return fail(MSSM_ERR_INVALID_ARG, "GATED_STEP_ROWS takes 0, 1, 2 or 4");
+      if (value != 0 && value != 1 && value != 2)
+        return fail(MSSM_ERR_INVALID_ARG, "GATED_STEP_ROWS takes 0, 1 or 2");
       g_step_rows = int(value);
       return MSSM_OK;
     case MSSM_OPT_W4_PLAN:
@@ -1456,6 +1456,8 @@ mssm_status mssm_gated_state_update(mssm_tensor* state, const mssm_tensor* x, co
     if (t)
       vec &= (t->stride[1] == 1 || Dd == 1) && (Bt == 1 || t->stride[0] % 4 == 0) &&
              reinterpret_cast<uintptr_t>(t->data) % (4 * size_t(esize(t->dtype))) == 0;
+  for (const mssm_tensor* t : {lam, r_bias, i_bias})
+    if (t) vec &= (t->stride[0] == 1 || Dd == 1) && aligned16(t->data);
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");

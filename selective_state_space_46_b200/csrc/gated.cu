@@ -39,8 +39,8 @@ static cudaError_t step_r(const GatedStepArgs& a, cudaStream_t s) {
 
 template <typename T>
 static cudaError_t step_t(const GatedStepArgs& a, bool vec, int rows, cudaStream_t s) {
-  if (!vec) return rows > 1 ? step_r<T, 1, 4>(a, s) : step_r<T, 1, 1>(a, s);
-  return rows > 2 ? step_r<T, 4, 4>(a, s) : rows > 1 ? step_r<T, 4, 2>(a, s) : step_r<T, 4, 1>(a, s);
+  if (!vec) return rows > 1 ? step_r<T, 1, 2>(a, s) : step_r<T, 1, 1>(a, s);
+  return rows > 1 ? step_r<T, 4, 2>(a, s) : step_r<T, 4, 1>(a, s);
 }
 
 cudaError_t launch_gated_step(const GatedStepArgs& a, bool vec, int rows, int dtype, cudaStream_t s) {

@@ -48,7 +48,7 @@ cudaError_t launch_scan_bwd(const BwdArgs& a, int dtype, bool has_z, cudaStream_
 // and a cluster).  The backward pass is followed by the sum of the batch's row sums when a.part is given.
 cudaError_t launch_gated_scan(const GatedArgs& a, int warps, int dtype, cudaStream_t s);
 cudaError_t launch_gated_bwd(const GatedArgs& a, int warps, int dtype, cudaStream_t s);
-// `vec`: 4 channels a thread (every pointer and row stride allows it); `rows`: batch rows a thread, 1, 2 or 4.
+// `vec`: 4 channels a thread (every pointer and row stride allows it); `rows`: batch rows a thread, 1 or 2.
 cudaError_t launch_gated_step(const GatedStepArgs& a, bool vec, int rows, int dtype, cudaStream_t s);
 // 4-bit linear map: the layout of a weight, and the product.
 cudaError_t launch_w4_pack(const W4PackArgs& a, int scale_dtype, cudaStream_t s);

@@ -220,6 +220,14 @@ __global__ void __launch_bounds__(32 * W) w4_linear_kernel(const W4Args p) {
     on[n] = m < p.M;
     xr[n] = static_cast<const T*>(p.x) + (on[n] ? m : 0) * p.x_sm + warp * kW4K + 8 * c;
   }
+  // tokens behind the last one are zeros, which nothing overwrites
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+    if (!on[n])
+      for (int k = 0; k < kSlots; ++k)
+        for (int e = 0; e < 2 * int(Ring::kXPart / 512); ++e)
+          *reinterpret_cast<uint4*>(s_mem + warp * Ring::kWarp + k * Ring::kSlot + Ring::kX + 2 * n * Ring::kXPart + e * 512 + lane * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
   const unsigned ring = unsigned(__cvta_generic_to_shared(s_mem)) + warp * Ring::kWarp, ring_end = ring + Ring::kWarp;
   // the pointers are those of the block that is asked for next
   int asked = warp;
@@ -307,8 +315,7 @@ __global__ void __launch_bounds__(32 * W) w4_linear_kernel(const W4Args p) {
         }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        XFrag<T> xf{};
-        if (on[n]) xf = x_frag<T>(at + Ring::kX + (2 * n + h) * Ring::kXPart + lane * 16);
+        const XFrag<T> xf = x_frag<T>(at + Ring::kX + (2 * n + h) * Ring::kXPart + lane * 16);
 #pragma unroll
         for (int t = 0; t < TT; ++t)
 #pragma unroll

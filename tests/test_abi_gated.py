@@ -198,7 +198,7 @@ def test_cpu_tensors_are_refused():
 
 def test_plan_options(lib):  # noqa: F811
     for opt, good, bad in ((9, (1, 2, 4, 8, 0), (-1, 3, 16)), (10, (1, 2, 4, 8, 0), (-1, 3, 16)), (11, (2, 8, 16, 0), (-1, 1, 4)),
-                           (12, (1, 2, 4, 0), (-1, 3, 8))):
+                           (12, (1, 2, 0), (-1, 3, 4))):
         lib.mssm_set_option.argtypes = [ctypes.c_int, ctypes.c_int64]
         for v in bad:
             assert lib.mssm_set_option(opt, v) == INVALID

@@ -577,11 +577,11 @@ def test_outputs_given_and_left_out(cuda_device):
         m.gated_scan_fwd(d["x"][0], d["r"], d["i"], d["lam"])
 
 
-@pytest.mark.parametrize("rows", [1, 2, 4])
+@pytest.mark.parametrize("rows", [1, 2])
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("shape", [(1, 4), (7, 12), (5, 13), (64, 260)])
 def test_every_step_plan(cuda_device, rows, io, shape):
-    """The decode step with 1, 2 and 4 batch rows a thread, whatever the automatic choice is, and replayed."""
+    """The decode step with 1 and 2 batch rows a thread, whatever the automatic choice is, and replayed."""
     import selective_state_space_46_b200 as m
     p = ref.gated_inputs(*shape, 1, io, h0=True, seed=rows)
     d = tensors(p, io)
