@@ -815,6 +815,8 @@ __device__ __forceinline__ WinMap win_map(const f2_t (&a)[kH], const f2_t (&b)[k
   return m;
 }
 
+// 1x2048x131072 bf16 with z: 518 us from a cold L2 (5.2 TB/s, issue 70%), 1536x27048 packed without z: 129 us, 88
+// unpacked; 2x1536x2048 18.4 us a call.
 template <typename T, int W, bool Z, bool VL, bool CL>
 __global__ void __launch_bounds__(gated_threads(W), kScanWarps * 32 / gated_threads(W)) gated_scan_kernel(const GatedArgs p) {
   __shared__ CarrySmem<W> sm;
@@ -956,6 +958,7 @@ __global__ void __launch_bounds__(gated_threads(W), kScanWarps * 32 / gated_thre
 // The row is swept forward once, keeping the state before every tile, then backwards tile by tile,
 // recomputing the states inside the tile: the second read finds the row in L2.  A row of one tile is
 // read once.
+// 8x5120x4096 bf16 with z: 774 us from a cold L2 (3.9 TB/s, issue 64%); 2x1536x2048 41 us a call.
 template <typename T, int W, bool Z, bool VL, bool CL>
 __global__ void __launch_bounds__(gated_threads(W), kBwdWarps * 32 / gated_threads(W)) gated_bwd_kernel(const GatedArgs p) {
   __shared__ CarrySmem<W> sm;

@@ -185,7 +185,9 @@ __device__ __forceinline__ void x_ask(unsigned to, const T* x, int k, int K, boo
 // their own scale.  Every lane has its 16 bytes of the next blocks, their scales and its x on the way into its
 // own places of shared memory (no other lane reads them, so the copies' own order is all the
 // synchronisation).  One token is bound by the instructions that unpack the codes as much as by the stream
-// of weights: 60 a block of 1024 codes, beside those of the loop and of x, which two tiles share.
+// of weights: 60 a block of 1024 codes, beside those of the loop and of x, which two tiles share.  Warp-level
+// products of 16 x 8 x 16 suit 8 to 32 tokens; a tile of 128 rows in tensor memory would stay mostly empty.
+// 1x5120x20480 bf16: 22.6 us a call (2.4 TB/s, ALU pipe 63%); 32x5120x20480: 53 us with the launch.
 template <typename T, typename S, int NT, int TT, bool HALF, bool ZERO>
 struct W4Ring {
   static constexpr int kSets = HALF ? 2 : 1;
