@@ -16,10 +16,10 @@
 #include <cuda_runtime.h>
 
 #include "device_common.cuh"
+#include "seq_walk.cuh"
 
 namespace mssm {
 
-constexpr int kGs = 8;             // steps per thread
 constexpr int kStepThreads = 128;  // of a CTA of the decode step
 constexpr float kResetA = -0.0f;   // the decay of a sequence's first step: composes to "ignore what came before"
 
@@ -384,96 +384,6 @@ __device__ __forceinline__ unsigned misalign(const T* p) {
   return unsigned(reinterpret_cast<uintptr_t>(p) & 15u);
 }
 
-// ---------------------------------------------------------------- packed sequences
-
-// The largest j in [0, S) with cu[j] <= t (0 if there is none), whatever the offsets hold.
-__device__ __forceinline__ int seq_of(const int* cu, int S, int t) {
-  int lo = 0, hi = S + 1;
-  while (lo < hi) {
-    const int mid = lo + (hi - lo) / 2;
-    if (__ldg(cu + mid) <= t) lo = mid + 1;
-    else hi = mid;
-  }
-  return max(min(lo - 1, S - 1), 0);
-}
-
-// What a window holds of the packed sequences: bit j for step t0 + j.
-struct SeqMask {
-  unsigned valid, first, last;  // inside a sequence; its first step; its last step
-  unsigned offs;                // steps with an offset
-  int below;                    // offsets before t0
-  bool twice;                   // some step has more than one offset (an empty sequence)
-};
-
-// A warp's walk through the offsets, 32 of them in its lanes.  Offsets that are out of order give wrong
-// sequences in [0, S) and an end to every loop.
-struct SeqWalk {
-  const int* cu;
-  int S, c0, cS;  // the first and last offset
-  int base, v;    // the lane's offset is number base + lane
-
-  __device__ __forceinline__ int get(int j) const { return j <= S ? __ldg(cu + j) : 0x7fffffff; }
-  __device__ __forceinline__ void start(const int* offsets, int n, int lane) {
-    cu = offsets;
-    S = n;
-    c0 = __ldg(cu);
-    cS = __ldg(cu + n);
-    base = 0;
-    v = get(lane);
-  }
-  // To the warp's steps [wt, wt + n), up or down the row.  Says whether they lie inside one sequence, with no
-  // first or last step.
-  __device__ __forceinline__ bool enter(int wt, int n, int lane) {
-    unsigned below = __ballot_sync(~0u, v < wt);
-    while (below == ~0u) {
-      base += 32;
-      v = get(base + lane);
-      below = __ballot_sync(~0u, v < wt);
-    }
-    while (below == 0u && base > 0) {
-      base -= 32;
-      v = get(base + lane);
-      below = __ballot_sync(~0u, v < wt);
-      if (below == ~0u) break;
-    }
-    const int before = base + __popc(below);
-    return !__any_sync(~0u, v >= wt && v <= wt + n) && below != ~0u && before >= 1 && before <= S;
-  }
-  __device__ __forceinline__ SeqMask masks(int wt, int t0, int L, int lane) const {
-    SeqMask m{0u, 0u, 0u, 0u, 0, false};
-    constexpr unsigned kAll = (1u << kGs) - 1u;
-    const int lo = max(max(c0, 0) - t0, 0), hi = min(min(cS, L) - t0, kGs);
-    if (hi > lo) m.valid = (kAll >> (kGs - hi)) & ~((1u << lo) - 1u);
-    const int te = wt + 32 * kGs;
-    m.below = base + __popc(__ballot_sync(~0u, v < wt));
-    int o32 = v;
-    for (int at = base;;) {
-      unsigned in = __ballot_sync(~0u, o32 >= wt && o32 <= te);
-      while (in) {
-        const int o = __shfl_sync(~0u, o32, __ffs(in) - 1) - t0;
-        in &= in - 1;
-        if (o < 0) ++m.below;
-        if (o >= 0 && o < kGs) {
-          m.twice |= m.offs >> o & 1u;
-          m.offs |= 1u << o;
-        }
-        if (o >= 1 && o <= kGs) m.last |= 1u << (o - 1);
-      }
-      if (__any_sync(~0u, o32 > te)) break;
-      at += 32;
-      o32 = get(at + lane);
-    }
-    m.first = m.offs & m.valid;
-    m.last &= m.valid;
-    return m;
-  }
-  // the sequence of step t0 + k
-  __device__ __forceinline__ int seq(const SeqMask& m, int t0, int k) const {
-    if (m.twice) return seq_of(cu, S, t0 + k);
-    return max(min(m.below + __popc(m.offs & ((2u << k) - 1u)) - 1, S - 1), 0);
-  }
-};
-
 // ---------------------------------------------------------------- composing affine maps
 
 // (a, b) after (pa, pb): h -> a (pa h + pb) + b.  With packed sequences a negative-zero a is a reset.
@@ -606,12 +516,6 @@ __device__ __forceinline__ void check_offsets(const int* cu, int S, int L, unsig
 // 8x5120x4096 bf16: 901 / 819 / 901 us (fewer registers spill, fewer warps leave the issue slots idle).
 constexpr int kScanWarps = 24, kBwdWarps = 16;
 constexpr int gated_threads(int W) { return W == 1 ? 128 : 32 * W; }
-
-// the steps of a plain row's window that lie inside the row
-__device__ __forceinline__ unsigned row_mask(int t0, int L) {
-  const int lo = max(-t0, 0), hi = min(L - t0, kGs);
-  return hi > lo ? ((1u << kGs) - 1u) >> (kGs - hi) & ~((1u << lo) - 1u) : 0u;
-}
 
 // Where a CTA's warp works: W warps of a CTA share a row, with CL the CTAs of a cluster do; with W == 1 every
 // warp has its own.
@@ -849,7 +753,7 @@ __global__ void __launch_bounds__(gated_threads(W), kScanWarps * 32 / gated_thre
   if (!VL && p.h0) h = p.h0[bt * p.h0_sb + d * p.h0_sd];
   SeqWalk walk;
   if (VL) {
-    walk.start(p.cu, p.S, lane);
+    walk.start(p.cu, p.S, p.L, lane);
     if (p.last)
       for (int j = at.wr * 32 + lane; j < p.S; j += 32 * W * at.split)
         if (p.cu[j] >= p.cu[j + 1])
@@ -865,8 +769,8 @@ __global__ void __launch_bounds__(gated_threads(W), kScanWarps * 32 / gated_thre
     bool whole = inner;
     if (VL) whole = walk.enter(wt, 32 * kGs, lane) && whole;
     if (!whole) {
-      if (VL) m = walk.masks(wt, t0, p.L, lane);
-      else m.valid = row_mask(t0, p.L);
+      if (VL) m = walk.masks(wt, t0, lane);
+      else m.valid = steps_inside(t0, 0, p.L);
     }
     float h0_first = 0.0f;  // of the window's first sequence start, asked for early
     if (VL && m.first && p.h0) h0_first = p.h0[int64_t(walk.seq(m, t0, __ffs(m.first) - 1)) * p.h0_sb + d * p.h0_sd];
@@ -1007,7 +911,7 @@ __global__ void __launch_bounds__(gated_threads(W), kBwdWarps * 32 / gated_threa
   else if (ntiles > 0) fetch_all(lane0);
   SeqWalk walk;
   if (VL) {
-    walk.start(p.cu, p.S, lane);
+    walk.start(p.cu, p.S, p.L, lane);
     if (p.dh0)
       for (int j = wr * 32 + lane; j < p.S; j += 32 * W * split)
         if (p.cu[j] >= p.cu[j + 1])
@@ -1024,8 +928,8 @@ __global__ void __launch_bounds__(gated_threads(W), kBwdWarps * 32 / gated_threa
     whole = inner_at(wt);
     if (VL) whole = walk.enter(wt, 32 * kGs, lane) && whole;
     if (!whole) {
-      if (VL) m = walk.masks(wt, wt + lane * kGs, p.L, lane);
-      else m.valid = row_mask(wt + lane * kGs, p.L);
+      if (VL) m = walk.masks(wt, wt + lane * kGs, lane);
+      else m.valid = steps_inside(wt + lane * kGs, 0, p.L);
     }
     h0_first = 0.0f;
     if (VL && m.first && p.h0)
