@@ -333,7 +333,7 @@ mssm_status mssm_causal_conv1d_update(mssm_tensor *conv_state, const mssm_tensor
  *                left unwritten.  Offsets outside [0, T] or decreasing ones are reported as
  *                MSSM_ERR_INVALID_ARG by mssm_get_error; the outputs are then undefined.
  * No workspace, and the same inputs in rows equally far from a 16-byte boundary give the
- * same bits.  L below 2^31 - 2^16.
+ * same bits.  L and the number of packed sequences below 2^31 - 2^16.
  */
 typedef struct {
     int32_t struct_size;

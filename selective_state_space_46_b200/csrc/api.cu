@@ -1249,8 +1249,9 @@ mssm_status gated_prepare(const mssm_tensor* x, const mssm_tensor* r, const mssm
                   (long long)Bt);
     S = cu->shape[0] - 1;
   }
-  if (Bt > INT32_MAX || Dd > INT32_MAX || L > INT32_MAX - (1 << 16) || S > INT32_MAX - 2)
-    return fail(MSSM_ERR_UNSUPPORTED, "Bt, D, L and the sequence count must each fit in 31 bits");
+  // the kernels step through a row, and through the offsets, by up to 2^14 at a time
+  if (Bt > INT32_MAX || Dd > INT32_MAX || L > INT32_MAX - (1 << 16) || S > INT32_MAX - (1 << 16))
+    return fail(MSSM_ERR_UNSUPPORTED, "Bt and D must fit in 31 bits, L and the sequence count be below 2^31 - 2^16");
   if (Bt * Dd > int64_t(INT32_MAX) || S * Dd > int64_t(INT32_MAX))
     return fail(MSSM_ERR_UNSUPPORTED, "Bt * D (or the sequence count * D) must fit in 31 bits");
   const int64_t s_sd[2] = {S, Dd};

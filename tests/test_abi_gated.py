@@ -97,6 +97,15 @@ def test_sizes_beyond_the_index_types_are_refused(lib):  # noqa: F811
     assert bwd(lib, gated_args(1, 1, (1 << 23) + 1)) == UNSUPPORTED
 
 
+@pytest.mark.parametrize("call", [fwd, bwd])
+def test_more_sequences_than_the_kernels_count_are_refused(lib, call):  # noqa: F811
+    """The loops over the offsets add their stride to an index of 31 bits."""
+    S = (1 << 31) - (1 << 16)
+    a = gated_args(1, 1, 32, S)
+    a["ext"] = Ext(ctypes.sizeof(Ext), 8.0, None, ctypes.pointer(mk([S + 1], I32)))
+    assert call(lib, a) == UNSUPPORTED, last_error(lib)
+
+
 def test_nothing_to_do_is_no_error(lib):  # noqa: F811
     for shape in ((0, 8, 32), (2, 0, 32)):
         assert fwd(lib, gated_args(*shape)) == 0
