@@ -4,12 +4,14 @@
 #include <Python.h>
 
 #include <algorithm>
+#include <utility>
 
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/utils/object_ptr.h>
 
 #include "mssm.h"
 
@@ -70,7 +72,7 @@ PyObject* describe(PyObject* const* args, Py_ssize_t n) {
     return nullptr;
   }
   int device = -1;
-  PyObject* out = PyTuple_New(n);
+  THPObjectPtr out(PyTuple_New(n));
   if (!out) return nullptr;
   for (Py_ssize_t j = 1; j < n; ++j) {
     PyObject* item = nullptr;
@@ -80,21 +82,15 @@ PyObject* describe(PyObject* const* args, Py_ssize_t n) {
     } else if (fill(args[j], block[j - 1], device)) {
       item = PyLong_FromVoidPtr(&block[j - 1]);
     }
-    if (!item) {
-      Py_DECREF(out);
-      return nullptr;
-    }
-    PyTuple_SET_ITEM(out, j, item);
+    if (!item) return nullptr;
+    PyTuple_SET_ITEM(out.get(), j, item);
   }
   PyObject* index = nullptr;
   if (device < 0) PyErr_SetString(PyExc_ValueError, "no tensor given");
   else index = PyLong_FromLong(device);
-  if (!index) {
-    Py_DECREF(out);
-    return nullptr;
-  }
-  PyTuple_SET_ITEM(out, 0, index);
-  return out;
+  if (!index) return nullptr;
+  PyTuple_SET_ITEM(out.get(), 0, index);
+  return out.release();
 }
 
 // Descriptors of a call's tensors, and the call itself on the device's current stream.
@@ -109,9 +105,9 @@ struct Call {
     ok = fill(arg, d[used], device);
     return ok ? &d[used++] : nullptr;
   }
-  // the output given, or (new reference in `made`) a new one
+  // the output given, or a new one
   template <typename F>
-  mssm_tensor* out(PyObject* arg, PyObject*& made, F make) {
+  mssm_tensor* out(PyObject* arg, THPObjectPtr& made, F make) {
     if (!ok) return nullptr;
     if (arg == Py_None) {
       made = THPVariable_Wrap(make());
@@ -120,23 +116,20 @@ struct Call {
       Py_INCREF(arg);
       made = arg;
     }
-    return const_cast<mssm_tensor*>(ok ? in(made) : nullptr);
+    return const_cast<mssm_tensor*>(ok ? in(made.get()) : nullptr);
   }
+  // Owns `made`, as every reference here is owned: an allocation that fails part way raises a C++ exception, and
+  // the outputs made before it must not outlive the call.
   template <typename F>
-  PyObject* run(PyObject* made, F f) {
-    if (!ok) {
-      Py_XDECREF(made);
-      return nullptr;
-    }
+  PyObject* run(THPObjectPtr made, F f) {
+    if (!ok) return nullptr;
     c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(device));
     void* stream = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream();
     mssm_status st;
     Py_BEGIN_ALLOW_THREADS
     st = f(stream);
     Py_END_ALLOW_THREADS
-    if (st == MSSM_OK) return made;
-    Py_DECREF(made);
-    return PyLong_FromLong(long(st));
+    return st == MSSM_OK ? made.release() : PyLong_FromLong(long(st));
   }
 };
 
@@ -153,7 +146,7 @@ PyObject* step(PyObject* const* args, Py_ssize_t n) {
   auto* state = const_cast<mssm_tensor*>(call.in(args[1]));
   const mssm_tensor *x = call.in(args[2]), *r = call.in(args[3]), *i = call.in(args[4]), *lam = call.in(args[5]),
                     *rb = call.in(args[6]), *ib = call.in(args[7]), *z = call.in(args[8]);
-  PyObject* made = nullptr;
+  THPObjectPtr made;
   if (call.ok && !x) {
     PyErr_SetString(PyExc_TypeError, "x: expected a tensor");
     return nullptr;
@@ -162,7 +155,7 @@ PyObject* step(PyObject* const* args, Py_ssize_t n) {
     const at::Tensor& t = THPVariable_Unpack(args[2]);
     return at::empty(t.sizes(), t.options().requires_grad(false));
   });
-  return call.run(made, [&](void* s) { return fn(state, x, r, i, lam, rb, ib, z, float(c), out, s); });
+  return call.run(std::move(made), [&](void* s) { return fn(state, x, r, i, lam, rb, ib, z, float(c), out, s); });
 }
 
 // scan(function, x, r, i, lam, r_bias, i_bias, z, decay scale, h0, cu_seqlens, out, last_state, whether to return it)
@@ -187,11 +180,10 @@ PyObject* scan(PyObject* const* args, Py_ssize_t n) {
   }
   const at::Tensor& x = THPVariable_Unpack(args[1]);
   const int64_t seqs = ext.cu_seqlens ? std::max<int64_t>(ext.cu_seqlens->shape[0] - 1, 0) : x.size(0);
-  PyObject* both = PyTuple_New(2);
+  THPObjectPtr both(PyTuple_New(2)), out_made, last_made;
   if (!both) return nullptr;
-  PyObject *out_made = nullptr, *last_made = nullptr;
   mssm_tensor* out = call.out(args[11], out_made, [&] { return at::empty(x.sizes(), x.options().requires_grad(false)); });
-  PyTuple_SET_ITEM(both, 0, out_made);
+  PyTuple_SET_ITEM(both.get(), 0, out_made.release());
   mssm_tensor* last = nullptr;
   if (want || args[12] != Py_None) {
     last = call.out(args[12], last_made, [&] {
@@ -201,8 +193,8 @@ PyObject* scan(PyObject* const* args, Py_ssize_t n) {
     Py_INCREF(Py_None);
     last_made = Py_None;
   }
-  PyTuple_SET_ITEM(both, 1, last_made);
-  return call.run(both, [&](void* s) { return fn(t[0], t[1], t[2], t[3], t[4], t[5], t[6], &ext, out, last, s); });
+  PyTuple_SET_ITEM(both.get(), 1, last_made.release());
+  return call.run(std::move(both), [&](void* s) { return fn(t[0], t[1], t[2], t[3], t[4], t[5], t[6], &ext, out, last, s); });
 }
 
 // scan_bwd(function, x, r, i, lam, r_bias, i_bias, z, decay scale, h0, cu_seqlens, dout, dlast_state) -> (dx, dr, di,
@@ -227,13 +219,13 @@ PyObject* scan_bwd(PyObject* const* args, Py_ssize_t n) {
   }
   const at::Tensor& x = THPVariable_Unpack(args[1]);
   const auto like = x.options().requires_grad(false), f32 = like.dtype(at::kFloat);
-  PyObject* made = PyTuple_New(8);
+  THPObjectPtr made(PyTuple_New(8));
   if (!made) return nullptr;
   mssm_tensor* g[8];
   for (int k = 0; k < 8; ++k) {
     // dz, the biases' gradients and dh0 come with their inputs
     const bool on = k == 3 ? t[6] != nullptr : k == 5 ? t[4] != nullptr : k == 6 ? t[5] != nullptr : k == 7 ? ext.h0 != nullptr : true;
-    PyObject* one = nullptr;
+    THPObjectPtr one;
     if (on) {
       g[k] = call.out(Py_None, one, [&] {
         if (k < 4) return at::empty(x.sizes(), like);
@@ -245,7 +237,7 @@ PyObject* scan_bwd(PyObject* const* args, Py_ssize_t n) {
       Py_INCREF(Py_None);
       one = Py_None;
     }
-    PyTuple_SET_ITEM(made, k, one);
+    PyTuple_SET_ITEM(made.get(), k, one.release());
   }
   mssm_tensor ws{};
   at::Tensor sums;
@@ -254,7 +246,7 @@ PyObject* scan_bwd(PyObject* const* args, Py_ssize_t n) {
     ws = mssm_tensor{sums.numel() ? sums.data_ptr() : nullptr, MSSM_F32, 3, {3, x.size(0), x.size(1), 0},
                      {sums.stride(0), sums.stride(1), sums.stride(2), 0}};
   }
-  return call.run(made, [&](void* s) {
+  return call.run(std::move(made), [&](void* s) {
     return fn(t[0], t[1], t[2], t[3], t[4], t[5], t[6], &ext, dout, dlast, g[0], g[1], g[2], g[3], g[4], g[5], g[6], g[7],
               sums.defined() ? &ws : nullptr, s);
   });
@@ -272,7 +264,7 @@ PyObject* linear(PyObject* const* args, Py_ssize_t n) {
   Call call;
   const mssm_tensor *x = call.in(args[1]), *q = call.in(args[2]), *s = call.in(args[3]), *z = call.in(args[4]),
                     *b = call.in(args[6]);
-  PyObject* made = nullptr;
+  THPObjectPtr made;
   if (call.ok && !x) {
     PyErr_SetString(PyExc_TypeError, "x: expected a tensor");
     return nullptr;
@@ -281,7 +273,7 @@ PyObject* linear(PyObject* const* args, Py_ssize_t n) {
     const at::Tensor& t = THPVariable_Unpack(args[1]);
     return at::empty({t.size(0), outputs}, t.options().requires_grad(false));
   });
-  return call.run(made, [&](void* stream) { return fn(x, q, s, z, group, b, out, stream); });
+  return call.run(std::move(made), [&](void* stream) { return fn(x, q, s, z, group, b, out, stream); });
 }
 
 // C++ exceptions (out of memory, a tensor without storage) become the Python ones that torch raises
