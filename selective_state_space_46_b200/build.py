@@ -79,10 +79,8 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
-def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    build_marshal(force, verbose)
-    if not force and up_to_date():
-        return LIB
+def compile_objects(force: bool = False, verbose: bool = False, extra_flags=()) -> list:
+    """Compiles every source whose object is missing or out of date; returns all objects."""
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
 
@@ -113,9 +111,16 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     todo = [src for src in srcs if stale(src)]
     with ThreadPoolExecutor(max_workers=max(1, min(len(todo), os.cpu_count() or 1))) as ex:
         list(ex.map(compile_one, todo))
-    objs = [os.path.join(BUILD_DIR, os.path.basename(src).replace(".cu", ".o")) for src in srcs]
+    return [os.path.join(BUILD_DIR, os.path.basename(src).replace(".cu", ".o")) for src in srcs]
+
+
+def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
+    build_marshal(force, verbose)
+    if not force and up_to_date():
+        return LIB
+    objs = compile_objects(force, verbose, extra_flags)
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
+    cmd = [_nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -35,6 +35,25 @@ cudaError_t device_error_word(unsigned int** out);
 void forget_device_addresses();
 // Incremented by forget_device_addresses: caches of per-device setup compare against it.
 int device_address_generation();
+
+// Lets `kernel` use `bytes` of dynamic shared memory (above the 48 KB default), once per
+// device, and again after mssm_shutdown (a device reset drops it).  set_gen: the caller's
+// own per-device record for this kernel (the address generation it was set in, + 1).
+template <typename K>
+cudaError_t opt_in_smem(K kernel, int bytes, int (&set_gen)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  const int gen = device_address_generation() + 1;
+  if (set_gen[dev] != gen) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    set_gen[dev] = gen;
+  }
+  return cudaSuccess;
+}
+
 // bulk: the state is one contiguous [rows][16] range (bulk-copy kernel), else one thread per row.
 enum class DecodePath { kStream, kBulkTile, kPerRow };
 cudaError_t launch_state_update(const DecodeArgs& a, int dtype, bool has_z, DecodePath path, cudaStream_t s);

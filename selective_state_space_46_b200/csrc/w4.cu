@@ -7,14 +7,9 @@ template <typename T, typename S, int NT, int TT, int W, bool HALF, bool ZERO>
 static cudaError_t w4_run(const W4Args& a, cudaStream_t s) {
   constexpr size_t smem = w4_smem<T, S, NT, TT, W, HALF, ZERO>();
   const auto kernel = w4_linear_kernel<T, S, NT, TT, W, HALF, ZERO>;
-  if (smem > 48 * 1024) {  // once for every device; the caller holds the library's lock
-    static uint64_t allowed = 0;
-    int dev = -1;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess && !(dev < 64 && (allowed >> dev & 1u))) {
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-      if (e == cudaSuccess && dev < 64) allowed |= uint64_t(1) << dev;
-    }
+  if (smem > 48 * 1024) {
+    static int set_gen[64] = {};  // one record per kernel instantiation
+    const cudaError_t e = opt_in_smem(kernel, int(smem), set_gen);
     if (e != cudaSuccess) return e;
   }
   const dim3 g(unsigned((a.tiles + TT - 1) / TT), unsigned((a.M + 8 * NT - 1) / (8 * NT)));

@@ -1,0 +1,74 @@
+"""What the library launches, without a GPU: its own host code against a runtime that records (tests/fake_cudart.cpp)."""
+import importlib.util
+import json
+import os
+import subprocess
+import sys
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def fake(tmp_path_factory):
+    spec = importlib.util.spec_from_file_location(
+        "_mssm_build", os.path.join(ROOT, "selective_state_space_46_b200", "build.py"))
+    build = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(build)
+    so = str(tmp_path_factory.mktemp("fake") / "libfake.so")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(build._nvcc()))), "include")
+    subprocess.run([os.environ.get("CXX", "g++"), "-std=c++17", "-fPIC", "-shared", "-Wl,-Bsymbolic", "-Wl,--no-undefined",
+                    "-I" + cuda, os.path.join(ROOT, "tests", "fake_cudart.cpp"), *build.compile_objects(), "-o", so], check=True)
+    return so
+
+
+PRELUDE = """
+import ctypes, json, sys
+sys.path[:0] = [{tests!r}, {root!r}]
+lib = ctypes.CDLL({so!r})
+lib.fake_kernel.restype = lib.mssm_last_error.restype = ctypes.c_char_p
+from test_abi_host import mk
+F32, BF16, I32, U8 = 0, 1, 2, 3
+V = ctypes.c_void_p
+
+def ref(t):
+    return None if t is None else ctypes.byref(t)
+
+def last():
+    v = (ctypes.c_uint * 5)()
+    lib.fake_last(v)
+    return dict(zip(("grid", "grid_y", "threads", "smem", "cluster"), v), kernel=lib.fake_kernel().decode(), count=lib.fake_launches())
+
+def linear(M, K, N, group, dt=BF16, zeros=False):
+    lib.mssm_w4_packed_sizes.argtypes = [ctypes.c_int64] * 3 + [ctypes.POINTER(ctypes.c_int64)] * 2
+    lib.mssm_w4_linear.argtypes = [V] * 4 + [ctypes.c_int64] + [V] * 3
+    q, s = ctypes.c_int64(), ctypes.c_int64()
+    assert lib.mssm_w4_packed_sizes(N, K, group, q, s) == 0
+    st = lib.mssm_w4_linear(ref(mk([M, K], dt)), ref(mk([q.value], I32)), ref(mk([s.value], dt)),
+                            ref(mk([s.value], U8)) if zeros else None, group, None, ref(mk([M, N], dt)), None)
+    return st
+"""
+
+
+def run(so, body):
+    """`body`, which leaves a JSON-able `result`, in a process that has the recording library alone."""
+    code = PRELUDE.format(tests=os.path.join(ROOT, "tests"), root=ROOT, so=so) + body + "\nprint(json.dumps(result))\n"
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stderr
+    return json.loads(r.stdout.splitlines()[-1])
+
+
+def test_linear_launches_after_shutdown_and_reset(fake):
+    """A device reset drops the kernels' shared-memory limits; mssm_shutdown before it makes the library set them again."""
+    got = run(fake, """
+result = []
+for device in (0, 3, 0):
+    lib.fake_device(device)
+    for again in range(2):
+        result += [linear(3, 1001, 193, 32, F32), linear(24, 999, 300, 96, zeros=True), linear(1, 5120, 20480, 128)]
+    result.append(last()["smem"] > 48 * 1024)
+    lib.mssm_shutdown()
+    lib.fake_reset()
+""")
+    assert got == ([0] * 6 + [True]) * 3
