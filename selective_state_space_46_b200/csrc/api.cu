@@ -1299,7 +1299,10 @@ GatedShape gated_shape(int64_t rows, int64_t L, bool backward, int sms) {
          L >= 8 * step * 4 * g.split)
     g.split *= 2;
   if (g_gated_warps) g.warps = g_gated_warps, g.split = 1;
-  if (g_gated_split) g.split = g_gated_split;
+  if (g_gated_split) {
+    g.split = g_gated_split;
+    while (rows * g.split > INT32_MAX) g.split /= 2;  // the grid's limit
+  }
   if (g.split > 1) g.warps = 8;
   return g;
 }

@@ -72,3 +72,23 @@ for device in (0, 3, 0):
     lib.fake_reset()
 """)
     assert got == ([0] * 6 + [True]) * 3
+
+
+def test_a_forced_split_keeps_every_row(fake):
+    """Rows times CTAs a row stay within a grid, and every row keeps its CTAs."""
+    got = run(fake, """
+result = []
+lib.mssm_set_option.argtypes = [ctypes.c_int, ctypes.c_int64]
+for D in (4, (1 << 28) - 1, (1 << 28) + 5, (1 << 29) + 8, (1 << 30) + 8, (1 << 31) - 1):
+    wide = [mk([1, D, 1], BF16) for _ in range(4)]
+    for k, t in enumerate(wide):
+        t.data = (1 << 40) * (k + 1)
+    lam = mk([D], F32, [0])
+    for split in (0, 2, 8):
+        assert lib.mssm_set_option(10, split) == 0
+        st = lib.mssm_gated_scan_fwd(ref(wide[0]), ref(wide[1]), ref(wide[2]), ref(lam), None, None, None, None, ref(wide[3]), None, None)
+        l = last()
+        per = 4 if l["threads"] == 128 and l["cluster"] == 1 else 1
+        result.append([st, l["grid"] % l["cluster"], l["grid"] // l["cluster"] * per >= D])
+""")
+    assert got == [[0, 0, True]] * 18
