@@ -40,11 +40,24 @@ if not os.path.exists(lib_path):
     raise ImportError(f"{lib_path} is missing: build it with `python selective_state_space_46_b200/build.py` "
                       "(nvcc, sm_100a); there is no fallback implementation")
 _lib = ctypes.CDLL(lib_path)
+
+
+class _Missing:
+    """Stands for the descriptor writer where it cannot be loaded: the operators that use it say so when they are called."""
+
+    def __init__(self, cause):
+        self._cause = cause
+
+    def __getattr__(self, name):
+        raise ImportError("the binding's descriptor writer (_marshal.so), which the gated recurrence and the 4-bit linear map "
+                          "use, is missing or was built for another torch: build it with "
+                          "`python selective_state_space_46_b200/build.py`") from self._cause
+
+
 try:
     from . import _marshal
 except ImportError as e:
-    raise ImportError("the binding's descriptor writer (_marshal.so) is missing or was built for another torch: build it "
-                      "with `python selective_state_space_46_b200/build.py`") from e
+    _marshal = _Missing(e)
 
 MSSM_F32, MSSM_BF16 = 0, 1
 MSSM_OK, MSSM_ERR_INVALID_ARG, MSSM_ERR_UNSUPPORTED, MSSM_ERR_CUDA, MSSM_ERR_TIMEOUT = 0, 1, 2, 3, 4

@@ -8,7 +8,9 @@ would load the library it is meant to build.
 Each .cu file is compiled to an object in parallel, then linked into a shared
 library next to this file.  The CUDA runtime is linked statically, so loading
 the library needs no GPU (only calling into it does).  The Python binding's
-descriptor writer (csrc/marshal.cpp) becomes _marshal.so beside it.
+descriptor writer (csrc/marshal.cpp) becomes _marshal.so beside it; where that
+cannot be built (it takes a C++ compiler and a torch with CUDA), the library still
+is, and every operator that does not use it runs.
 """
 from __future__ import annotations
 
@@ -17,6 +19,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -115,10 +118,16 @@ def compile_objects(force: bool = False, verbose: bool = False, extra_flags=()) 
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    build_marshal(force, verbose)
-    if not force and up_to_date():
-        return LIB
-    objs = compile_objects(force, verbose, extra_flags)
+    if force or not up_to_date():
+        link(compile_objects(force, verbose, extra_flags), verbose)
+    try:
+        build_marshal(force, verbose)
+    except (RuntimeError, ImportError, OSError) as e:  # no C++ compiler, or no torch with CUDA and its headers
+        warnings.warn(f"the library is built, but the gated recurrence and the 4-bit linear map need _marshal.so from Python: {e}")
+    return LIB
+
+
+def link(objs, verbose: bool = False) -> str:
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [_nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     if verbose:
