@@ -49,22 +49,22 @@ struct SeqWalk {
     v = get(lane);
   }
   // To the warp's steps [wt, wt + n), up or down the row.  Says whether they lie inside one sequence, with no
-  // first or last step.
+  // first or last step.  Neighbouring blocks of offsets share one, so that the last offset in front of the steps and
+  // the first behind it are always in the lanes together, also at a block's end.
   __device__ __forceinline__ bool enter(int wt, int n, int lane) {
     unsigned below = __ballot_sync(~0u, v < wt);
     while (below == ~0u) {
-      base += 32;
+      base += 31;
       v = get(base + lane);
       below = __ballot_sync(~0u, v < wt);
     }
     while (below == 0u && base > 0) {
-      base -= 32;
+      base -= 31;
       v = get(base + lane);
       below = __ballot_sync(~0u, v < wt);
-      if (below == ~0u) break;
     }
     const int before = base + __popc(below);
-    return !__any_sync(~0u, v >= wt && v <= wt + n) && below != ~0u && before >= 1 && before <= S;
+    return !__any_sync(~0u, v >= wt && v <= wt + n) && before >= 1 && before <= S;
   }
   __device__ __forceinline__ SeqMask masks(int wt, int t0, int lane) const {
     SeqMask m{steps_inside(t0, c0, cS), 0u, 0u, 0u, 0, false};

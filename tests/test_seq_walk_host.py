@@ -77,6 +77,18 @@ def test_masks_of_random_sequences(host):
             check_against_definition(host, cu, L, int(rng.integers(0, 8)), WINDOW, bool(rng.integers(2)))
 
 
+@pytest.mark.parametrize("back", [False, True])
+@pytest.mark.parametrize("S", [1, 30, 31, 32, 33, 63, 64, 65, 96])
+def test_windows_inside_one_sequence_are_whole(host, S, back):
+    """Every window without a boundary takes the way without masks, whichever sequence it lies in."""
+    for stride in (WINDOW, 2 * WINDOW):
+        cu = np.arange(S + 1) * 1000
+        t, whole, valid, starts, ends, _ = walk(host, cu, int(cu[-1]), 0, stride, back)
+        one = valid.all(1) & ~starts.any(1) & ~ends.any(1)
+        assert one.sum() >= S // (stride // WINDOW)
+        np.testing.assert_array_equal(whole, one)
+
+
 WILD = [[0, INT_MIN], [0, INT_MIN, INT_MIN], [INT_MAX, INT_MAX], [INT_MAX, 50], [INT_MIN, INT_MAX], [INT_MAX, INT_MIN],
         [INT_MIN, 20, INT_MAX], [0, 60], [-3, 20, 50], [50, 40, 30, 20, 10, 0], [70, 80, 90], [0, INT_MAX, 0, INT_MIN, 50],
         [0] + [INT_MIN] * 40 + [50], [0] + [INT_MAX] * 40 + [50], list(range(70, 0, -1))]
