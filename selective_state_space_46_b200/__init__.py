@@ -380,7 +380,8 @@ class _allocating_on:
 
     def __init__(self, stream, device):
         if stream is not None and not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=device)
+            # torch takes the address 0 for no address, and then makes a stream of its own
+            stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
         self.guard = None if stream is None else torch.cuda.stream(stream)
 
     def __enter__(self):
@@ -495,20 +496,11 @@ def gated_scan_fwd(x, r, i, lam, r_bias=None, i_bias=None, z=None, c=8.0, h0=Non
     ``i`` (both before bias and sigmoid), decay rate ``c * softplus(lam)`` and optional silu gate ``z``,
     from ``h0`` [S, D] when given, over packed sequences when ``cu_seqlens`` is.  Returns ``(out,
     last_state)``; steps outside every packed sequence are not written."""
-    if stream is None:
-        both = _marshal.scan(_SCAN, x, r, i, lam, r_bias, i_bias, z, c, h0, cu_seqlens, out, last_state, return_last_state)
-        if type(both) is int:
-            _check(both)
-        return both
-    if out is None or (last_state is None and return_last_state):
-        with _allocating_on(stream, x.device):
-            if out is None:
-                out = torch.empty_like(x, memory_format=torch.contiguous_format)
-            if last_state is None and return_last_state:
-                seqs = x.shape[0] if cu_seqlens is None else cu_seqlens.shape[0] - 1
-                last_state = torch.empty(seqs, x.shape[1], device=x.device, dtype=torch.float32)
-    mssm_gated_scan_fwd(x, r, i, lam, r_bias, i_bias, z, out, last_state, c, h0, cu_seqlens, stream)
-    return out, last_state
+    both = _marshal.scan(_SCAN, x, r, i, lam, r_bias, i_bias, z, c, h0, cu_seqlens, out, last_state, return_last_state,
+                         stream)
+    if type(both) is int:
+        _check(both)
+    return both
 
 
 def gated_scan_bwd(x, r, i, lam, r_bias=None, i_bias=None, z=None, dout=None, c=8.0, h0=None, cu_seqlens=None,
@@ -516,41 +508,19 @@ def gated_scan_bwd(x, r, i, lam, r_bias=None, i_bias=None, z=None, dout=None, c=
     """Allocate the gradients with torch and run the gated recurrence's backward pass: ``dx, dr, di, dz,
     dlam, dr_bias, di_bias, dh0`` (None where the input is; ``dh0`` is given with ``h0``).  Gradients at steps
     outside every packed sequence are not written."""
-    if stream is None:
-        g = _marshal.scan_bwd(_SCAN_BWD, x, r, i, lam, r_bias, i_bias, z, c, h0, cu_seqlens, dout, dlast_state)
-        if type(g) is int:
-            _check(g)
-        return dict(zip(_GRADS, g))
-    device, f32 = x.device, torch.float32
-    batch, dim = x.shape[0], x.shape[1]
-    with _allocating_on(stream, device):
-        def new():
-            return torch.empty_like(x, memory_format=torch.contiguous_format)
-
-        g = dict(dx=new(), dr=new(), di=new(), dz=None if z is None else new(),
-                 dlam=torch.empty(dim, device=device, dtype=f32),
-                 dr_bias=None if r_bias is None else torch.empty(dim, device=device, dtype=f32),
-                 di_bias=None if i_bias is None else torch.empty(dim, device=device, dtype=f32),
-                 dh0=None if h0 is None else torch.empty(h0.shape, device=device, dtype=f32))
-        ws = torch.empty(3, batch, dim, device=device, dtype=f32) if batch > 1 else None
-    mssm_gated_scan_bwd(x, r, i, lam, r_bias, i_bias, z, dout, dlast_state, g["dx"], g["dr"], g["di"], g["dz"],
-                        g["dlam"], g["dr_bias"], g["di_bias"], g["dh0"], ws, c, h0, cu_seqlens, stream)
-    return g
+    g = _marshal.scan_bwd(_SCAN_BWD, x, r, i, lam, r_bias, i_bias, z, c, h0, cu_seqlens, dout, dlast_state, stream)
+    if type(g) is int:
+        _check(g)
+    return dict(zip(_GRADS, g))
 
 
 def gated_state_update(state, x, r, i, lam, r_bias=None, i_bias=None, z=None, c=8.0, out=None,
                        stream=None) -> torch.Tensor:
     """One decode step of the gated recurrence on ``x`` [Bt, D] (``state`` [Bt, D] updated in place);
     returns ``out``."""
-    if stream is None:
-        out = _marshal.step(_STEP, state, x, r, i, lam, r_bias, i_bias, z, c, out)
-        if type(out) is int:
-            _check(out)
-        return out
-    if out is None:
-        with _allocating_on(stream, x.device):
-            out = torch.empty_like(x, memory_format=torch.contiguous_format)
-    mssm_gated_state_update(state, x, r, i, lam, r_bias, i_bias, z, out, c, stream)
+    out = _marshal.step(_STEP, state, x, r, i, lam, r_bias, i_bias, z, c, out, stream)
+    if type(out) is int:
+        _check(out)
     return out
 
 
@@ -587,14 +557,8 @@ def w4_linear(x, weight: W4Weight, bias=None, out=None, stream=None) -> torch.Te
         raise ValueError(f"x: expected [M, {weight.in_features}], got {list(x.shape)}")
     if out is not None and out.shape != (x.shape[0], weight.out_features):
         raise ValueError(f"out: expected [{x.shape[0]}, {weight.out_features}], got {list(out.shape)}")
-    if stream is None:
-        out = _marshal.linear(_LINEAR, x, weight.qweight, weight.qscales, weight.qzeros, weight.group_size, bias,
-                              weight.out_features, out)
-        if type(out) is int:
-            _check(out)
-        return out
-    if out is None:
-        with _allocating_on(stream, x.device):
-            out = torch.empty(x.shape[0], weight.out_features, device=x.device, dtype=x.dtype)
-    mssm_w4_linear(x, weight.qweight, weight.qscales, weight.qzeros, weight.group_size, bias, out, stream)
+    out = _marshal.linear(_LINEAR, x, weight.qweight, weight.qscales, weight.qzeros, weight.group_size, bias,
+                          weight.out_features, out, stream)
+    if type(out) is int:
+        _check(out)
     return out

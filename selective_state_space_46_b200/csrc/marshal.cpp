@@ -93,17 +93,27 @@ PyObject* describe(PyObject* const* args, Py_ssize_t n) {
   return out.release();
 }
 
-// Descriptors of a call's tensors, and the call itself on the device's current stream.
+// Descriptors of a call's tensors, and the call itself, on a stream of their device.
 struct Call {
   mssm_tensor d[20];
   int device = -1;
   int used = 0;
+  c10::cuda::OptionalCUDAStreamGuard stream;
   // null for None; `ok` turns false with a Python error
   bool ok = true;
   const mssm_tensor* in(PyObject* arg) {
     if (!ok || arg == Py_None) return nullptr;
     ok = fill(arg, d[used], device);
     return ok ? &d[used++] : nullptr;
+  }
+  // A torch stream, a stream's address, or None for the device's current one: the outputs allocated from here on
+  // belong to it.
+  void on(PyObject* arg) {
+    if (!ok || arg == Py_None || device < 0) return;
+    THPObjectPtr address(PyLong_Check(arg) ? Py_NewRef(arg) : PyObject_GetAttrString(arg, "cuda_stream"));
+    void* at = address ? PyLong_AsVoidPtr(address.get()) : nullptr;
+    if (PyErr_Occurred()) ok = false;
+    else stream.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(at), static_cast<c10::DeviceIndex>(device)));
   }
   // the output given, or a new one
   template <typename F>
@@ -124,19 +134,19 @@ struct Call {
   PyObject* run(THPObjectPtr made, F f) {
     if (!ok) return nullptr;
     c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(device));
-    void* stream = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream();
+    void* at = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream();
     mssm_status st;
     Py_BEGIN_ALLOW_THREADS
-    st = f(stream);
+    st = f(at);
     Py_END_ALLOW_THREADS
     return st == MSSM_OK ? made.release() : PyLong_FromLong(long(st));
   }
 };
 
-// step(function, state, x, r, i, lam, r_bias, i_bias, z, decay scale, out) -> out, or the status of a failed call
+// step(function, state, x, r, i, lam, r_bias, i_bias, z, decay scale, out, stream) -> out, or the status of a failed call
 PyObject* step(PyObject* const* args, Py_ssize_t n) {
-  if (n != 11) {
-    PyErr_SetString(PyExc_TypeError, "step takes 11 arguments");
+  if (n != 12) {
+    PyErr_SetString(PyExc_TypeError, "step takes 12 arguments");
     return nullptr;
   }
   const auto fn = reinterpret_cast<decltype(&mssm_gated_state_update)>(PyLong_AsVoidPtr(args[0]));
@@ -151,6 +161,7 @@ PyObject* step(PyObject* const* args, Py_ssize_t n) {
     PyErr_SetString(PyExc_TypeError, "x: expected a tensor");
     return nullptr;
   }
+  call.on(args[11]);
   mssm_tensor* out = call.out(args[10], made, [&] {
     const at::Tensor& t = THPVariable_Unpack(args[2]);
     return at::empty(t.sizes(), t.options().requires_grad(false));
@@ -158,11 +169,11 @@ PyObject* step(PyObject* const* args, Py_ssize_t n) {
   return call.run(std::move(made), [&](void* s) { return fn(state, x, r, i, lam, rb, ib, z, float(c), out, s); });
 }
 
-// scan(function, x, r, i, lam, r_bias, i_bias, z, decay scale, h0, cu_seqlens, out, last_state, whether to return it)
-// -> (out, last_state), or the status of a failed call
+// scan(function, x, r, i, lam, r_bias, i_bias, z, decay scale, h0, cu_seqlens, out, last_state, whether to return it,
+// stream) -> (out, last_state), or the status of a failed call
 PyObject* scan(PyObject* const* args, Py_ssize_t n) {
-  if (n != 14) {
-    PyErr_SetString(PyExc_TypeError, "scan takes 14 arguments");
+  if (n != 15) {
+    PyErr_SetString(PyExc_TypeError, "scan takes 15 arguments");
     return nullptr;
   }
   const auto fn = reinterpret_cast<decltype(&mssm_gated_scan_fwd)>(PyLong_AsVoidPtr(args[0]));
@@ -180,6 +191,8 @@ PyObject* scan(PyObject* const* args, Py_ssize_t n) {
   }
   const at::Tensor& x = THPVariable_Unpack(args[1]);
   const int64_t seqs = ext.cu_seqlens ? std::max<int64_t>(ext.cu_seqlens->shape[0] - 1, 0) : x.size(0);
+  call.on(args[14]);
+  if (!call.ok) return nullptr;
   THPObjectPtr both(PyTuple_New(2)), out_made, last_made;
   if (!both) return nullptr;
   mssm_tensor* out = call.out(args[11], out_made, [&] { return at::empty(x.sizes(), x.options().requires_grad(false)); });
@@ -197,11 +210,11 @@ PyObject* scan(PyObject* const* args, Py_ssize_t n) {
   return call.run(std::move(both), [&](void* s) { return fn(t[0], t[1], t[2], t[3], t[4], t[5], t[6], &ext, out, last, s); });
 }
 
-// scan_bwd(function, x, r, i, lam, r_bias, i_bias, z, decay scale, h0, cu_seqlens, dout, dlast_state) -> (dx, dr, di,
-// dz, dlam, dr_bias, di_bias, dh0), or the status of a failed call
+// scan_bwd(function, x, r, i, lam, r_bias, i_bias, z, decay scale, h0, cu_seqlens, dout, dlast_state, stream) ->
+// (dx, dr, di, dz, dlam, dr_bias, di_bias, dh0), or the status of a failed call
 PyObject* scan_bwd(PyObject* const* args, Py_ssize_t n) {
-  if (n != 13) {
-    PyErr_SetString(PyExc_TypeError, "scan_bwd takes 13 arguments");
+  if (n != 14) {
+    PyErr_SetString(PyExc_TypeError, "scan_bwd takes 14 arguments");
     return nullptr;
   }
   const auto fn = reinterpret_cast<decltype(&mssm_gated_scan_bwd)>(PyLong_AsVoidPtr(args[0]));
@@ -219,6 +232,8 @@ PyObject* scan_bwd(PyObject* const* args, Py_ssize_t n) {
   }
   const at::Tensor& x = THPVariable_Unpack(args[1]);
   const auto like = x.options().requires_grad(false), f32 = like.dtype(at::kFloat);
+  call.on(args[13]);
+  if (!call.ok) return nullptr;
   THPObjectPtr made(PyTuple_New(8));
   if (!made) return nullptr;
   mssm_tensor* g[8];
@@ -252,10 +267,10 @@ PyObject* scan_bwd(PyObject* const* args, Py_ssize_t n) {
   });
 }
 
-// linear(function, x, qweight, qscales, qzeros, group, bias, outputs, out) -> out, or the status of a failed call
+// linear(function, x, qweight, qscales, qzeros, group, bias, outputs, out, stream) -> out, or the status of a failed call
 PyObject* linear(PyObject* const* args, Py_ssize_t n) {
-  if (n != 9) {
-    PyErr_SetString(PyExc_TypeError, "linear takes 9 arguments");
+  if (n != 10) {
+    PyErr_SetString(PyExc_TypeError, "linear takes 10 arguments");
     return nullptr;
   }
   const auto fn = reinterpret_cast<decltype(&mssm_w4_linear)>(PyLong_AsVoidPtr(args[0]));
@@ -269,6 +284,7 @@ PyObject* linear(PyObject* const* args, Py_ssize_t n) {
     PyErr_SetString(PyExc_TypeError, "x: expected a tensor");
     return nullptr;
   }
+  call.on(args[9]);
   mssm_tensor* out = call.out(args[8], made, [&] {
     const at::Tensor& t = THPVariable_Unpack(args[1]);
     return at::empty({t.size(0), outputs}, t.options().requires_grad(false));
@@ -292,15 +308,15 @@ PyCFunction method() {
 PyMethodDef methods[] = {
     {"describe", method<describe>(), METH_FASTCALL, "describe(block, *tensors) -> (device index, *descriptor addresses)"},
     {"step", method<step>(), METH_FASTCALL,
-     "step(function, state, x, r, i, lam, r_bias, i_bias, z, decay_scale, out) -> out, or a failed call's status"},
+     "step(function, state, x, r, i, lam, r_bias, i_bias, z, decay_scale, out, stream) -> out, or a failed call's status"},
     {"scan", method<scan>(), METH_FASTCALL,
-     "scan(function, x, r, i, lam, r_bias, i_bias, z, decay_scale, h0, cu_seqlens, out, last_state, want_last) -> "
+     "scan(function, x, r, i, lam, r_bias, i_bias, z, decay_scale, h0, cu_seqlens, out, last_state, want_last, stream) -> "
      "(out, last_state), or a failed call's status"},
     {"scan_bwd", method<scan_bwd>(), METH_FASTCALL,
-     "scan_bwd(function, x, r, i, lam, r_bias, i_bias, z, decay_scale, h0, cu_seqlens, dout, dlast_state) -> gradients, or "
+     "scan_bwd(function, x, r, i, lam, r_bias, i_bias, z, decay_scale, h0, cu_seqlens, dout, dlast_state, stream) -> gradients, or "
      "a failed call's status"},
     {"linear", method<linear>(), METH_FASTCALL,
-     "linear(function, x, qweight, qscales, qzeros, group, bias, outputs, out) -> out, or a failed call's status"},
+     "linear(function, x, qweight, qscales, qzeros, group, bias, outputs, out, stream) -> out, or a failed call's status"},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

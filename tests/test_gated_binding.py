@@ -73,3 +73,63 @@ def test_a_refused_call_keeps_nothing(cuda_device):
             m.gated_state_update(x[..., 0], x[..., 0], x[..., 0], x[..., 0], lam[:3])
     gc.collect()
     assert torch.cuda.memory_allocated() == before
+
+
+def streams():
+    side = torch.cuda.Stream()
+    return (None, side, side.cuda_stream, torch.cuda.default_stream(), 0)
+
+
+def test_errors_are_the_same_on_every_stream(cuda_device):
+    import selective_state_space_46_b200 as m
+    x, lam = inputs(2, 8, 64)
+    flat = x[..., 0].contiguous()
+    codes, scales = torch.zeros(16, 32, device="cuda", dtype=torch.uint8), torch.ones(16, 1, device="cuda")
+    weight = m.w4_pack(codes, scales, group_size=64)
+    for s in streams():
+        for bad in (x[0], x[None], lam):
+            with pytest.raises(ValueError, match="Bt, D, L"):
+                m.gated_scan_fwd(bad, x, x, lam, stream=s)
+            with pytest.raises(ValueError, match="Bt, D, L"):
+                m.gated_scan_bwd(bad, x, x, lam, dout=x, stream=s)
+        with pytest.raises(TypeError, match="expected a tensor"):
+            m.gated_state_update(flat, [1.0], flat, flat, lam, stream=s)
+        with pytest.raises(TypeError, match="expected a tensor"):
+            m.gated_scan_fwd(x, x, x, lam, cu_seqlens=[0, 64], stream=s)
+        with pytest.raises(ValueError, match="CUDA"):
+            m.gated_scan_fwd(x.cpu(), x, x, lam, stream=s)
+        with pytest.raises(m.MssmError):
+            m.gated_state_update(flat, x[..., 0, None], flat, flat, lam, stream=s)
+        with pytest.raises(m.MssmError):
+            m.gated_scan_bwd(x, x, x, lam, stream=s)
+        with pytest.raises(m.MssmError):
+            m.w4_linear(torch.zeros(2, 64, device="cuda"), weight, bias=lam, stream=s)
+
+
+def test_outputs_belong_to_the_stream_of_the_call(cuda_device):
+    """What a call allocates lies in its stream's part of the memory, so that freeing it orders with the call."""
+    import selective_state_space_46_b200 as m
+    x, lam = inputs(2, 40, 1 << 16)
+    flat = torch.randn(1, 1 << 22, device="cuda")
+    codes, scales = torch.zeros(1 << 21, 32, device="cuda", dtype=torch.uint8), torch.ones(1 << 21, 1, device="cuda")
+    weight = m.w4_pack(codes, scales, group_size=64)
+    tokens = torch.randn(1, 64, device="cuda")
+    torch.cuda.synchronize()
+
+    def owner(t):
+        for seg in torch.cuda.memory_snapshot():
+            if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+                return seg["stream"]
+        raise AssertionError("not in the allocator's memory")
+
+    for s in streams():
+        raw = 0 if s is None else s if isinstance(s, int) else s.cuda_stream
+        out, last = m.gated_scan_fwd(x, x, x, lam, stream=s)
+        g = m.gated_scan_bwd(x, x, x, lam, z=x, dout=x, h0=torch.zeros(2, 40, device="cuda"), stream=s)
+        step = m.gated_state_update(torch.zeros_like(flat), flat, flat, flat, flat[0], stream=s)
+        y = m.w4_linear(tokens, weight, stream=s)
+        packed = m.w4_pack(codes, scales, group_size=64, stream=s)
+        torch.cuda.synchronize()
+        made = [out, last, y, step, packed.qweight, packed.qscales] + [v for v in g.values() if v is not None]
+        assert {owner(t) for t in made} == {raw}
+        assert torch.cuda.current_stream() == torch.cuda.default_stream()
