@@ -73,11 +73,6 @@ __device__ __forceinline__ float rsqrt_approx(float x) {
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 __device__ __forceinline__ f2_t f2s(float v) { return f2(v, v); }
 
 // softplus and the logistic function of a per-channel parameter, once per row: the accurate
@@ -102,12 +97,21 @@ struct GatedRow {
 constexpr float kFastEnd = 0.125f;
 constexpr float kSeriesEnd = 0.25f;
 
+// A larger rate is put into the gate's exponent instead: 2^40 / (1 + e 2^40 / rate) is rate / (1 + e) to 2^-33 wherever
+// that is below 128, and above, a is 0 and beta 1 in any case.  So y, y h and y / beta stay finite, for an infinite rate too.
+constexpr float kMostRate = 1099511627776.0f;  // 2^40
+
 template <typename Args>
 __device__ __forceinline__ GatedRow gated_row(const Args& p, int d) {
   GatedRow w;
-  const float q = p.c * softplus_exact(p.lam[d * p.lam_s]), q2 = q * q;
-  w.rate = q;
+  float q = p.c * softplus_exact(p.lam[d * p.lam_s]);
   w.cr = p.rb ? -kLog2e * p.rb[d * p.rb_s] : 0.0f;
+  if (q > kMostRate) {
+    w.cr -= log2f(q * (1.0f / kMostRate));
+    q = kMostRate;
+  }
+  const float q2 = q * q;
+  w.rate = q;
   w.ci = p.ib ? -kLog2e * p.ib[d * p.ib_s] : 0.0f;
   w.slow = !(q < kFastEnd);
   w.a1 = -q;
