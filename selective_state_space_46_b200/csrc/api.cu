@@ -1590,14 +1590,17 @@ mssm_status mssm_w4_linear(const mssm_tensor* x, const mssm_tensor* qweight, con
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   std::lock_guard<std::mutex> lk(g_mu);
   // Two tiles of 16 outputs a CTA share the loop's and x's instructions, where that leaves every SM half a CTA
-  // or more; few tiles of a long row take more warps instead.  Device us (with 6 to 8 of launch) for 2 tiles /
-  // 8 warps / 16 warps, bf16: 1x5120x20480 27 / 29 / 31, 32x5120x20480 53 / 80 / 86, 16x5120x2560 14 / 16 / 18,
-  // 4x16384x2048 31 / 23 / 18, 1x16384x1024 25 / 21 / 16.
+  // or more (a CTA takes up to 32 tokens of bf16, 16 of fp32); few tiles of a long row take more warps instead.
+  // Device us for 2 tiles / 8 warps / 16 warps, weights from a rotation of four: bf16 1x5120x20480 21.6 / 24.1 / 26.9,
+  // 32x5120x20480 52.9 / 72.0 / 78.2, 16x5120x2560 8.5 / 10.2 / 10.9, 32x2560x1536 7.6 / 6.4 / 6.6, 1x16384x2048
+  // 16.7 / 12.6 / 10.2; fp32 1x5120x20480 40.0 / 53.2 / 55.1, 24x2560x1536 9.4 / 13.4 / 14.5, 16x2560x1536 9.3 / 8.4 /
+  // 8.3, 32x16384x2048 45.8 / 70.8 / 68.9, 16x16384x2048 45.8 / 40.8 / 35.2.
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
   const int64_t sms = device_state(dev)->sm_count;
-  int choice = w.tiles * ((M + 31) / 32) >= sms ? 2 : w.blocks >= 128 ? 16 : 8;
+  const int64_t most = dt == MSSM_BF16 ? 32 : 16;
+  int choice = w.tiles * ((M + most - 1) / most) >= sms ? 2 : w.blocks >= 128 ? 16 : 8;
   if (g_w4_plan) choice = g_w4_plan;
   const mssm::W4Plan plan = choice == 2 ? mssm::W4Plan{2, 8} : mssm::W4Plan{1, choice};
   e = tracked(MSSM_KERNEL_W4_LINEAR, s, [&] { return mssm::launch_w4_linear(a, plan, dt, qscales->dtype, s); });

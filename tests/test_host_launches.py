@@ -92,3 +92,20 @@ for D in (4, (1 << 28) - 1, (1 << 28) + 5, (1 << 29) + 8, (1 << 30) + 8, (1 << 3
         result.append([st, l["grid"] % l["cluster"], l["grid"] // l["cluster"] * per >= D])
 """)
     assert got == [[0, 0, True]] * 18
+
+
+def test_linear_plan_counts_the_ctas_it_launches(fake):
+    """Two tiles of outputs a CTA wherever one tile a CTA would give every SM one or more, in either type."""
+    got = run(fake, """
+result = []
+for dt in (F32, BF16):
+    for M in (1, 8, 16, 17, 24, 32, 33, 64, 100):
+        for N in (64, 1536, 2048, 2352, 2368, 5120):
+            assert linear(M, 2560, N, 128, dt) == 0
+            l = last()
+            tiles = (N + 15) // 16
+            two = l["grid"] == (tiles + 1) // 2
+            assert two or l["grid"] == tiles
+            result.append([dt, M, N, two, tiles * l["grid_y"] >= 148])
+""")
+    assert [r for r in got if r[3] != r[4]] == []
