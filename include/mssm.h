@@ -356,6 +356,7 @@ mssm_status mssm_gated_scan_fwd(const mssm_tensor *x, const mssm_tensor *r, cons
  *   dh0              [S, D] f32 or NULL (also without h0: the gradient at the zero state)
  *   workspace        [3, Bt, D] f32, dense: the rows' parts of dlam and the biases'
  *                    gradients, which are then added in batch order; NULL when Bt is 1
+ * dlam, dr_bias and di_bias are sums in fp32, in a fixed order.
  * The states are recomputed, never stored.  Gradients at steps outside every packed
  * sequence are left unwritten.  Bits as for the forward scan.  L may reach 2^23.
  */
@@ -385,7 +386,7 @@ mssm_status mssm_gated_state_update(mssm_tensor *state, const mssm_tensor *x, co
  * mssm_w4_pack lays a weight out once in the order in which the product reads it:
  *   codes    [N, (K + 1) / 2] u8: input 2j in the low nibble of byte j, 2j + 1 in the high
  *   scales   [N, G] f32|bf16, G = ceil(K / group); the last group may be short
- *   zeros    [N, G] u8, values 0..15, or NULL: 8 everywhere
+ *   zeros    [N, G] u8, values 0..15 (of larger ones the low 4 bits count), or NULL: 8 everywhere
  *   group    a positive multiple of 32
  *   qweight, qscales, qzeros: dense 1-dim i32, dtype of scales, u8 (given exactly when
  *            zeros is), of the sizes that mssm_w4_packed_sizes returns
@@ -393,10 +394,12 @@ mssm_status mssm_gated_state_update(mssm_tensor *state, const mssm_tensor *x, co
  *   x        [M, K] bf16|f32, K stride 1;  out [M, N] dtype of x, any strides
  *   bias     [N] f32 or NULL
  *   N, K, group as packed (K and N are read from x and out)
- * Every group's sum and the sum over the groups are fp32; the products are exact.  The
- * inputs are split over warps, and for few outputs over the CTAs of a cluster, whose sums
- * are added in a fixed order: the same inputs give the same bits.  Any M is taken; the
- * kernels are laid out for a few tokens, and re-read the weight for every 32 of them.
+ * The products of a code and an input are exact.  They are added in fp32, 32 or 64 inputs of
+ * one group at a time by the tensor core (whose sum may truncate), then scaled and added to
+ * the output's sum in fp32; a sum of 64 inputs times 15 has to stay finite.  The inputs are
+ * split over the warps of a CTA, whose sums are added in a fixed order: the same inputs give
+ * the same bits.  M up to 524280; the kernels are laid out for a few tokens, and re-read the
+ * weight for every 32 of them (fp32 activations: 16).
  * K and N at least 1 and below 2^31 - 64.
  */
 mssm_status mssm_w4_packed_sizes(int64_t N, int64_t K, int64_t group, int64_t *qweight, int64_t *qscales);

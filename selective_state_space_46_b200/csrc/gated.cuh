@@ -88,7 +88,7 @@ struct GatedRow {
   float rate;          // c softplus(lam)
   float cr, ci;        // -log2(e) times the biases
   bool slow;           // some gate may take y = rate r to 1/8: CARE
-  // Polynomials of y on [0, 1/8] as polynomials of r, near-minimax fits with relative errors below 2^-25.
+  // Polynomials of y on [0, 1/8] as polynomials of r, near-minimax fits with relative errors below 2^-24.9.
   // (A decay of 0.9 to 0.999 at r = 1, the usual start, has a rate of 0.001 to 0.105.)
   float a1, a2, a3, a4;  // exp(-y) = 1 + a1 r + ...: a fit of (1 - exp(-y)) / y
   float p0, p1, p2, p3;  // sqrt(2 rate) P(y), P = sqrt((1 - exp(-2y)) / (2y))
@@ -723,8 +723,9 @@ __device__ __forceinline__ WinMap win_map(const f2_t (&a)[kH], const f2_t (&b)[k
   return m;
 }
 
-// 1x2048x131072 bf16 with z: 518 us from a cold L2 (5.2 TB/s, issue 70%), 1536x27048 packed without z: 129 us, 88
-// unpacked; 2x1536x2048 18.4 us a call.
+// 1x2048x131072 bf16 with z: 518 us from a cold L2 (5.2 TB/s, issue 70%), 542 to 580 back to back, at the clock under
+// that load; 1536x27048 packed without z: 128 us, 88 unpacked; 2x1536x2048 18.4 us a call.  Rates from 1/8 on:
+// 8x2048x4096 with z 152 us, 129 below.
 template <typename T, int W, bool Z, bool VL, bool CL>
 __global__ void __launch_bounds__(gated_threads(W), kScanWarps * 32 / gated_threads(W)) gated_scan_kernel(const GatedArgs p) {
   __shared__ CarrySmem<W> sm;
@@ -866,7 +867,8 @@ __global__ void __launch_bounds__(gated_threads(W), kScanWarps * 32 / gated_thre
 // The row is swept forward once, keeping the state before every tile, then backwards tile by tile,
 // recomputing the states inside the tile: the second read finds the row in L2.  A row of one tile is
 // read once.
-// 8x5120x4096 bf16 with z: 774 us from a cold L2 (3.9 TB/s, issue 64%); 2x1536x2048 41 us a call.
+// 8x5120x4096 bf16 with z: 774 us from a cold L2 (3.9 TB/s, issue 64%), 774 to 837 back to back (845 to 880 with rates
+// from 1/8 on); 2x1536x2048 41 us a call.
 template <typename T, int W, bool Z, bool VL, bool CL>
 __global__ void __launch_bounds__(gated_threads(W), kBwdWarps * 32 / gated_threads(W)) gated_bwd_kernel(const GatedArgs p) {
   __shared__ CarrySmem<W> sm;
