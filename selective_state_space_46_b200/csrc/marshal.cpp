@@ -110,7 +110,7 @@ struct Call {
   // belong to it.
   void on(PyObject* arg) {
     if (!ok || arg == Py_None || device < 0) return;
-    THPObjectPtr address(PyLong_Check(arg) ? Py_NewRef(arg) : PyObject_GetAttrString(arg, "cuda_stream"));
+    THPObjectPtr address(PyIndex_Check(arg) ? PyNumber_Index(arg) : PyObject_GetAttrString(arg, "cuda_stream"));
     void* at = address ? PyLong_AsVoidPtr(address.get()) : nullptr;
     if (PyErr_Occurred()) ok = false;
     else stream.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(at), static_cast<c10::DeviceIndex>(device)));

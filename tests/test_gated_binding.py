@@ -1,6 +1,7 @@
 """The binding of the gated recurrence and the 4-bit linear map: what a failed call leaves behind."""
 import gc
 
+import numpy as np
 import pytest
 import torch
 
@@ -77,7 +78,7 @@ def test_a_refused_call_keeps_nothing(cuda_device):
 
 def streams():
     side = torch.cuda.Stream()
-    return (None, side, side.cuda_stream, torch.cuda.default_stream(), 0)
+    return (None, side, side.cuda_stream, np.int64(side.cuda_stream), torch.cuda.default_stream(), 0)
 
 
 def test_errors_are_the_same_on_every_stream(cuda_device):
@@ -123,7 +124,7 @@ def test_outputs_belong_to_the_stream_of_the_call(cuda_device):
         raise AssertionError("not in the allocator's memory")
 
     for s in streams():
-        raw = 0 if s is None else s if isinstance(s, int) else s.cuda_stream
+        raw = 0 if s is None else s.cuda_stream if isinstance(s, torch.cuda.Stream) else int(s)
         out, last = m.gated_scan_fwd(x, x, x, lam, stream=s)
         g = m.gated_scan_bwd(x, x, x, lam, z=x, dout=x, h0=torch.zeros(2, 40, device="cuda"), stream=s)
         step = m.gated_state_update(torch.zeros_like(flat), flat, flat, flat, flat[0], stream=s)
